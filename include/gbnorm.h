@@ -78,8 +78,14 @@ typedef enum {
                            GBN_STATIC_WS_BYTES */
 } gbn_status;
 
-/* Layer selector of gbn_bwd_workspace_bytes. */
-typedef enum { GBN_OP_DYT = 0, GBN_OP_LAYERNORM = 1, GBN_OP_RMSNORM = 2 } gbn_op;
+/* Layer selector of gbn_bwd_workspace_bytes (GBN_OP_RMSNORM_ADD: both
+ * rmsnorm_add_bwd and rmsnorm_add_ckpt_bwd). */
+typedef enum {
+    GBN_OP_DYT = 0,
+    GBN_OP_LAYERNORM = 1,
+    GBN_OP_RMSNORM = 2,
+    GBN_OP_RMSNORM_ADD = 3
+} gbn_op;
 
 /* Human-readable name of a gbn_status value (static storage). */
 const char* gbn_status_string(int status);
@@ -281,6 +287,88 @@ int rmsnorm_bwd_rows(const void* x, const gbn_rows* xl, const void* dy, const gb
 int rmsnorm_bwd_static_ws(const void* x, const void* dy, const void* w, const float* rstd,
                           void* dx, void* dw, int64_t M, int64_t N, float eps, int xt, int wt,
                           cudaStream_t stream);
+
+/* --------------------------------- RMSNorm with the residual's addition
+ * The residual stream of a transformer: a block's output x is added to the
+ * stream res, the sum s is the new stream, and its RMSNorm feeds the next
+ * block.  With rx the rounding to x's type,
+ *   s = rx(x + res)                   in f32, rounded once
+ *   r = rsqrt(mean_j s^2 + eps)       over the stored s, in f32 (0 where the
+ *                                     sum of squares passes f32's range)
+ *   y = the expression `variant` of s r and w (gbn_rms_variant)
+ * so that s and y are those of an addition followed by rmsnorm_fwd_ex.
+ *
+ * Shared conventions (besides those at the top of this file)
+ *   x, res, s, dy, ds share the type xt; w is as in rmsnorm_fwd_ex.  x, res,
+ *   dy and ds may carry row layouts (gbn_rows, null for contiguous rows).
+ *   res may be null: then s is x itself, and the s output must be null too.
+ *   s may be null when only y is wanted, and may be the memory of x or of
+ *   res where that input is contiguous (an update in place); dx may be the
+ *   memory of ds on the same condition.  Other overlaps are not allowed.
+ *   rstd [M] f32 is nullable in the forwards and required in the backwards.
+ *
+ * 8-bit values.  An 8-bit type (gbn_q8) holds values with one f32 scale per
+ *   group of `group` columns (32, 64 or 128; the last group of a row may be
+ *   short) or per row (group 0): [M, ceil(N / group)] scales, row-major,
+ *   [M] for group 0.  An element stands for q * scale.  With qmax 448
+ *   (e4m3) or 127 (int8; -128 is never written), a the largest magnitude of
+ *   a group and every step one f32 operation,
+ *     scale = max(a (1 / qmax), 2^-100),   q = round(v (1 / scale)),
+ *   rounded to nearest even.  (The floor keeps 1 / scale finite: a group of
+ *   zeros holds zeros.)  A group with a NaN or an infinity gets a scale of
+ *   NaN or infinity, so that all of it reads back as NaN. */
+typedef enum { GBN_E4M3 = 8, GBN_INT8 = 9 } gbn_q8;
+
+/* s, y, rstd as above. */
+int rmsnorm_add_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                    const void* w, void* s, void* y, float* rstd, int64_t M, int64_t N, float eps,
+                    int xt, int wt, int variant, cudaStream_t stream);
+
+/* y in 8 bits: q [M, N] of type qt with its scales.  The 8-bit rounding is
+ *   the only one: y = w' s r is held in f32 before it (w' = w, or 1 + w for
+ *   GBN_RMS_GEMMA; GBN_RMS_CAST_FIRST equals GBN_RMS_WEIGHT_FIRST), with
+ *   scale = max(r max_j |w' s| (1 / qmax), 2^-100) and q = round(w' s
+ *   (r (1 / scale))). */
+int rmsnorm_add_quant_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                          const void* w, void* s, void* q, float* scale, float* rstd, int64_t M,
+                          int64_t N, int64_t group, float eps, int xt, int wt, int qt, int variant,
+                          cudaStream_t stream);
+
+/* rmsnorm_add_fwd that also leaves an activation checkpoint: c [M, N] of type
+ *   ct with its scales is s in 8 bits, the bits of act_pack8 on s. */
+int rmsnorm_add_ckpt_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                         const void* w, void* s, void* y, float* rstd, void* c, float* cscale,
+                         int64_t M, int64_t N, int64_t group, float eps, int xt, int wt, int ct,
+                         int variant, cudaStream_t stream);
+
+/* Backward.  dy is the gradient of y, ds that of s from the stream's other
+ *   readers (null: none).  With xhat = s r, dn and the terms of dw as in
+ *   rmsnorm_bwd_ex,
+ *     dx = rx(ds + r (dn - xhat mean_j(dn xhat)))
+ *   is the gradient of x and of res alike; dw [N] in w's type, nullable.
+ *   s may carry a row layout.  Workspace: GBN_OP_RMSNORM_ADD. */
+int rmsnorm_add_bwd(const void* s, const gbn_rows* sl, const void* dy, const gbn_rows* dyl,
+                    const void* ds, const gbn_rows* dsl, const void* w, const float* rstd,
+                    void* dx, void* dw, int64_t M, int64_t N, int xt, int wt, int variant,
+                    void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The same from a checkpoint of s: xhat = q (scale r).  Only dx and dw are
+ *   rounded, in every expression (xhat is not the forward's, so the forward's
+ *   rounding of it has no counterpart). */
+int rmsnorm_add_ckpt_bwd(const void* c, const float* cscale, const void* dy, const gbn_rows* dyl,
+                         const void* ds, const gbn_rows* dsl, const void* w, const float* rstd,
+                         void* dx, void* dw, int64_t M, int64_t N, int64_t group, int xt, int wt,
+                         int ct, int variant, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------ 8-bit activation checkpoints
+ * act_pack8: x [M, N] (xt) to c [M, N] (ct) and its scales; act_unpack8: the
+ *   values c stands for, rounded to xt.  For layers whose backward reads x
+ *   itself (dyt_bwd, layernorm_bwd) the checkpoint is unpacked in front of
+ *   it. */
+int act_pack8(const void* x, const gbn_rows* xl, void* c, float* cscale, int64_t M, int64_t N,
+              int64_t group, int xt, int ct, cudaStream_t stream);
+int act_unpack8(const void* c, const float* cscale, void* x, int64_t M, int64_t N, int64_t group,
+                int xt, int ct, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

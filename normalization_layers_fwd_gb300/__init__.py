@@ -12,16 +12,21 @@ gbn_rows layout and read in place; outputs are contiguous.
 """
 from ._lib import (  # noqa: F401
     GBN_BF16,
+    GBN_E4M3,
     GBN_F16,
     GBN_F32,
+    GBN_INT8,
     GBN_OP_DYT,
     GBN_OP_LAYERNORM,
     GBN_OP_RMSNORM,
+    GBN_OP_RMSNORM_ADD,
     GBN_RMS_CAST_FIRST,
     GBN_RMS_GEMMA,
     GBN_RMS_WEIGHT_FIRST,
     GBN_STATIC_WS_BYTES,
     GbnError,
+    act_pack8,
+    act_unpack8,
     dyt_bwd,
     dyt_fwd,
     fold_rows,
@@ -30,6 +35,11 @@ from ._lib import (  # noqa: F401
     layernorm_fwd,
     load,
     read_faults,
+    rmsnorm_add_bwd,
+    rmsnorm_add_ckpt_bwd,
+    rmsnorm_add_ckpt_fwd,
+    rmsnorm_add_fwd,
+    rmsnorm_add_quant_fwd,
     rmsnorm_bwd,
     rmsnorm_bwd_static_ws,
     rmsnorm_fwd,

@@ -14,6 +14,7 @@ fallback, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -22,13 +23,17 @@ import torch
 from . import build as _build
 
 GBN_F32, GBN_BF16, GBN_F16 = 0, 1, 2
-GBN_OP_DYT, GBN_OP_LAYERNORM, GBN_OP_RMSNORM = 0, 1, 2
+GBN_OP_DYT, GBN_OP_LAYERNORM, GBN_OP_RMSNORM, GBN_OP_RMSNORM_ADD = 0, 1, 2, 3
 GBN_OK = 0
 # RMSNorm expressions: Llama (weight after the cast), weight before the cast, Gemma (1 + w)
 GBN_RMS_CAST_FIRST, GBN_RMS_WEIGHT_FIRST, GBN_RMS_GEMMA = 0, 1, 2
 GBN_ESCRATCH = 6
 GBN_STATIC_WS_BYTES = 8 << 20  # size of the library's static scratch array
 SIZE_MAX = ctypes.c_size_t(-1).value
+
+# 8-bit types of quantised outputs and activation checkpoints
+GBN_E4M3, GBN_INT8 = 8, 9
+_DTYPES8 = {torch.float8_e4m3fn: GBN_E4M3, torch.int8: GBN_INT8}
 
 _DTYPES = {torch.float32: GBN_F32, torch.bfloat16: GBN_BF16, torch.float16: GBN_F16}
 
@@ -67,6 +72,17 @@ SIGNATURES = {
     "rmsnorm_fwd_rows": ([_P, _R, _P, _P, _P, _I64, _I64, _F, _I, _I, _I, _P], _I),
     "rmsnorm_bwd_rows": ([_P, _R, _P, _R, _P, _P, _P, _P, _I64, _I64, _F, _I, _I, _I, _P, _SZ,
                           _P], _I),
+    "rmsnorm_add_fwd": ([_P, _R, _P, _R, _P, _P, _P, _P, _I64, _I64, _F, _I, _I, _I, _P], _I),
+    "rmsnorm_add_quant_fwd": ([_P, _R, _P, _R, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I,
+                               _I, _I, _P], _I),
+    "rmsnorm_add_ckpt_fwd": ([_P, _R, _P, _R, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I,
+                              _I, _I, _I, _P], _I),
+    "rmsnorm_add_bwd": ([_P, _R, _P, _R, _P, _R, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _P, _SZ,
+                         _P], _I),
+    "rmsnorm_add_ckpt_bwd": ([_P, _P, _P, _R, _P, _R, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I,
+                              _I, _I, _P, _SZ, _P], _I),
+    "act_pack8": ([_P, _R, _P, _P, _I64, _I64, _I64, _I, _I, _P], _I),
+    "act_unpack8": ([_P, _P, _P, _I64, _I64, _I64, _I, _I, _P], _I),
 }
 
 _lock = threading.Lock()
@@ -356,3 +372,208 @@ def rmsnorm_bwd_static_ws(x, dy, w, rstd=None, eps=1e-6, need_dw=True):
                                         M, N, float(eps), _code(x), _code(w), _stream(x.device)),
            "rmsnorm_bwd_static_ws")
     return dx, dw
+
+
+# ------------------------------ RMSNorm with the residual's addition, 8 bits
+#
+# These calls may come from any thread, on any device and stream: they launch
+# on the inputs' device and its current stream, and a backward's workspace is
+# its own allocation, so calls on several streams, or captured into several
+# graphs, share nothing.
+
+def _call(name, device, *args):
+    fn = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != GBN_OK:
+        raise GbnError(st, name)
+
+
+def _act(t, name, like=None):
+    """(t or a contiguous copy, its layout, M, N) of an activation; like: the
+    tensor it must match in shape, type and device."""
+    if not t.is_cuda:
+        raise ValueError("activations must be CUDA tensors")
+    if like is None:
+        _code(t)
+        if t.dim() < 1:
+            raise ValueError("activations need at least one dimension")
+    elif t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must match in shape, dtype and device: {tuple(t.shape)} "
+                         f"{t.dtype} {t.device}, expected {tuple(like.shape)} {like.dtype} "
+                         f"{like.device}")
+    N = t.shape[-1]
+    M = t.numel() // N if N else 0
+    if t.is_contiguous():
+        return t, None, M, N
+    t, lay = row_layout(t)
+    return t, _lay(lay), M, N
+
+
+def _code8(dtype) -> int:
+    try:
+        return _DTYPES8[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported 8-bit dtype {dtype}: float8_e4m3fn or int8") from None
+
+
+def _scales(x, N, group):
+    """An empty tensor for x's scales: [..., ceil(N / group)], [..., 1] for rows."""
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"group is {group}: 0 (a scale per row), 32, 64 or 128 columns")
+    n = 1 if group == 0 else -(-N // group)
+    return torch.empty((*x.shape[:-1], n), dtype=torch.float32, device=x.device)
+
+
+def _add_inputs(x, residual, w, s):
+    """The forwards' inputs and the stream's output."""
+    x, xl, M, N = _act(x, "x")
+    w = _param(w, x, N, "w")
+    rl = None
+    if residual is None:
+        if s is not None:
+            raise ValueError("s is an output of the addition: without a residual the stream is x")
+        return x, xl, None, None, w, x, None, M, N
+    residual, rl, _, _ = _act(residual, "residual", x)
+    if s is None:
+        s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif (s.shape != x.shape or s.dtype != x.dtype or s.device != x.device
+          or not s.is_contiguous()):
+        raise ValueError("s must be contiguous and match x in shape, dtype and device")
+    return x, xl, residual, rl, w, s, s, M, N
+
+
+def rmsnorm_add_fwd(x, residual, w, eps=1e-6, save_rstd=True, variant=GBN_RMS_CAST_FIRST, s=None):
+    """(y, s, rstd): s = x + residual, rounded once to x's type, and y the
+    RMSNorm of s (variant as in rmsnorm_fwd).  residual None: s is x.  s: a
+    contiguous tensor that takes the sum; it may be x or residual itself."""
+    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if save_rstd else None
+    _call("rmsnorm_add_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
+          _ptr(y), _ptr(rstd), M, N, eps, _code(x), _code(w), variant)
+    return y, stream, rstd
+
+
+def rmsnorm_add_quant_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, group=0,
+                          save_rstd=True, variant=GBN_RMS_CAST_FIRST, s=None):
+    """(q, scale, s, rstd): rmsnorm_add_fwd with y in 8 bits (dtype
+    float8_e4m3fn or int8) and its f32 scales, one per row (group 0) or per
+    group of 32, 64 or 128 columns: y is q * scale.  y stays f32 up to the
+    8-bit rounding, so variants 0 and 1 are the same here."""
+    qt = _code8(dtype)
+    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
+    scale = _scales(x, N, group)
+    q = torch.empty(x.shape, dtype=dtype, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if save_rstd else None
+    _call("rmsnorm_add_quant_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
+          _ptr(q), _ptr(scale), _ptr(rstd), M, N, group, eps, _code(x), _code(w), qt, variant)
+    return q, scale, stream, rstd
+
+
+def rmsnorm_add_ckpt_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, group=128,
+                         variant=GBN_RMS_CAST_FIRST, s=None):
+    """(y, s, rstd, c, cscale): rmsnorm_add_fwd that also writes the 8-bit
+    checkpoint of s (act_pack8's c and cscale) in the same pass."""
+    ct = _code8(dtype)
+    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
+    cscale = _scales(x, N, group)
+    c = torch.empty(x.shape, dtype=dtype, device=x.device)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    _call("rmsnorm_add_ckpt_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
+          _ptr(y), _ptr(rstd), _ptr(c), _ptr(cscale), M, N, group, eps, _code(x), _code(w), ct,
+          variant)
+    return y, stream, rstd, c, cscale
+
+
+@functools.lru_cache(maxsize=4096)
+def _add_ws_bytes(M, N, xt, wt, index):
+    n = load().gbn_bwd_workspace_bytes(GBN_OP_RMSNORM_ADD, M, N, xt, wt, index)
+    if n == SIZE_MAX:
+        raise GbnError(1, "gbn_bwd_workspace_bytes")
+    return n
+
+
+def _add_grads(dy, ds, w, rstd, need_dw, M, N):
+    """The backwards' remaining inputs and outputs."""
+    w = _param(w, dy, N, "w")
+    rstd = _param(rstd, dy, M, "rstd")
+    if rstd.dtype != torch.float32:
+        raise TypeError("rstd must be float32")
+    dsl = None
+    if ds is not None:
+        ds, dsl, _, _ = _act(ds, "ds", dy)
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    dw = ws = None
+    n = 0
+    if need_dw:
+        dw = torch.empty(N, dtype=w.dtype, device=dy.device)
+        n = _add_ws_bytes(M, N, _code(dy), _code(w), dy.device.index)
+        ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
+    return w, rstd, ds, dsl, dx, dw, ws, n
+
+
+def rmsnorm_add_bwd(s, dy, w, rstd, ds=None, need_dw=True, variant=GBN_RMS_CAST_FIRST):
+    """(dx, dw): dx is the gradient of x and of the residual alike, ds (the
+    gradient of s from its other readers, None for none) included.  s and rstd
+    are the forward's."""
+    dy, dyl, M, N = _act(dy, "dy")
+    s, sl, _, _ = _act(s, "s", dy)
+    w, rstd, ds, dsl, dx, dw, ws, n = _add_grads(dy, ds, w, rstd, need_dw, M, N)
+    _call("rmsnorm_add_bwd", dy.device, _ptr(s), sl, _ptr(dy), dyl, _ptr(ds), dsl, _ptr(w),
+          _ptr(rstd), _ptr(dx), _ptr(dw), M, N, _code(dy), _code(w), variant, _ptr(ws), n)
+    return dx, dw
+
+
+def _packed(c, cscale, group, shape, device):
+    """An 8-bit tensor and its scales, checked and contiguous."""
+    ct = _code8(c.dtype)
+    if not c.is_cuda or c.shape != shape or c.device != device:
+        raise ValueError(f"the 8-bit tensor must be {tuple(shape)} on {device}")
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"group is {group}: 0 (a scale per row), 32, 64 or 128 columns")
+    n = 1 if group == 0 else -(-shape[-1] // group)
+    if (cscale.shape != (*shape[:-1], n) or cscale.dtype != torch.float32
+            or cscale.device != device):
+        raise ValueError(f"the scales must be float32 {(*shape[:-1], n)} on {device}")
+    return c.contiguous(), cscale.contiguous(), ct
+
+
+def rmsnorm_add_ckpt_bwd(c, cscale, dy, w, rstd, ds=None, group=128, need_dw=True,
+                         variant=GBN_RMS_CAST_FIRST):
+    """(dx, dw) like rmsnorm_add_bwd, from the 8-bit checkpoint of s (c, cscale
+    and group as rmsnorm_add_ckpt_fwd or act_pack8 made them) in place of s."""
+    dy, dyl, M, N = _act(dy, "dy")
+    c, cscale, ct = _packed(c, cscale, group, dy.shape, dy.device)
+    w, rstd, ds, dsl, dx, dw, ws, n = _add_grads(dy, ds, w, rstd, need_dw, M, N)
+    _call("rmsnorm_add_ckpt_bwd", dy.device, _ptr(c), _ptr(cscale), _ptr(dy), dyl, _ptr(ds), dsl,
+          _ptr(w), _ptr(rstd), _ptr(dx), _ptr(dw), M, N, group, _code(dy), _code(w), ct, variant,
+          _ptr(ws), n)
+    return dx, dw
+
+
+def act_pack8(x, dtype=torch.float8_e4m3fn, group=128):
+    """(c, cscale): x in 8 bits (float8_e4m3fn or int8) with f32 scales per row
+    (group 0) or per group of 32, 64 or 128 columns; x is about c * cscale."""
+    ct = _code8(dtype)
+    x, xl, M, N = _act(x, "x")
+    cscale = _scales(x, N, group)
+    c = torch.empty(x.shape, dtype=dtype, device=x.device)
+    _call("act_pack8", x.device, _ptr(x), xl, _ptr(c), _ptr(cscale), M, N, group, _code(x), ct)
+    return c, cscale
+
+
+def act_unpack8(c, cscale, dtype=torch.bfloat16, group=128):
+    """c * cscale in dtype: what act_pack8 (or a quantised output) stands for."""
+    if c.dim() < 1:
+        raise ValueError("activations need at least one dimension")
+    c, cscale, ct = _packed(c, cscale, group, c.shape, c.device)
+    x = torch.empty(c.shape, dtype=dtype, device=c.device)
+    N = c.shape[-1]
+    M = c.numel() // N if N else 0
+    _call("act_unpack8", c.device, _ptr(c), _ptr(cscale), _ptr(x), M, N, group, _code(x), ct)
+    return x

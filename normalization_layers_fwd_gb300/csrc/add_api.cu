@@ -1,0 +1,253 @@
+// add_api.cu -- the extern "C" entry points of the residual-stream operators:
+// argument checks and launches.  Nothing here allocates memory or
+// synchronizes.
+#include <cmath>
+#include <initializer_list>
+
+#include "addnorm.cuh"
+#include "gbnorm.h"
+#include "internal.h"
+
+namespace gbn {
+
+size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int, int sms)
+{
+    const size_t need = (size_t)add_bwd_general_rows(M, N, sms) * (size_t)N * sizeof(float);
+    return (need + 255) & ~(size_t)255;
+}
+
+}  // namespace gbn
+
+namespace {
+
+using gbn::RowSrc;
+
+bool dtype_ok(int t) { return t == gbn::kF32 || t == gbn::kBF16 || t == gbn::kF16; }
+bool q8_ok(int t) { return t == GBN_E4M3 || t == GBN_INT8; }
+bool group_ok(int64_t g) { return g == 0 || g == 32 || g == 64 || g == 128; }
+int elem_bytes(int t) { return t == gbn::kF32 ? 4 : 2; }
+
+bool aligned(int bytes, std::initializer_list<const void*> ps)
+{
+    for (const void* p : ps)
+        if ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0) return false;
+    return true;
+}
+
+// The rules of rmsnorm_fwd_ex: expression 0 with 16-bit activations takes a
+// weight of f32 or of their type.
+int norm_types(int xt, int wt, int variant)
+{
+    if (variant < GBN_RMS_CAST_FIRST || variant > GBN_RMS_GEMMA) return GBN_EINVAL;
+    if (!dtype_ok(xt) || !dtype_ok(wt)) return GBN_EDTYPE;
+    if (variant == GBN_RMS_CAST_FIRST && xt != GBN_F32 && wt != GBN_F32 && wt != xt)
+        return GBN_EDTYPE;
+    return GBN_OK;
+}
+
+// An activation input as the kernels take it; false for a bad layout.
+bool source(RowSrc& out, const void* p, const gbn_rows* l, int64_t M, int64_t N, int e)
+{
+    bool scattered = false;
+    out = RowSrc{};
+    out.p = static_cast<const unsigned char*>(p);
+    out.row_bytes = N * e;
+    out.total = M * N * e;
+    if (!gbn::host_layout_map(p ? l : nullptr, M, N, e, out.map, scattered)) return false;
+    out.scattered = scattered ? 1 : 0;
+    return true;
+}
+
+gbn::Q8 q8_of(void* v, const float* scale, int type, int64_t N, int64_t group)
+{
+    gbn::Q8 q{};
+    q.v = v;
+    q.scale = const_cast<float*>(scale);
+    q.type = type;
+    const bool row = group == 0 || group >= N;  // one group: the whole row
+    q.shift = row ? 31 : group == 32 ? 5 : group == 64 ? 6 : 7;
+    q.ng = row ? 1 : (int)((N + group - 1) / group);
+    return q;
+}
+
+int launch_status(cudaError_t e) { return e == cudaSuccess ? GBN_OK : GBN_ELAUNCH; }
+
+// Every forward: what is asked for is what is not null (w null: act_pack8).
+struct Fwd {
+    const void* x;
+    const gbn_rows* xl;
+    const void* res;
+    const gbn_rows* rl;
+    const void* w;
+    void *s, *y;
+    float* rstd;
+    gbn::Q8 q, c;
+    float eps;
+    int xt, wt, variant;
+};
+
+int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
+{
+    const int e = elem_bytes(f.xt);
+    if (!aligned(e, {f.x, f.res, f.s, f.y}) || !aligned(4, {f.rstd, f.q.scale, f.c.scale}))
+        return GBN_EINVAL;
+    gbn::FwdArgs a{};
+    if (!source(a.x, f.x, f.xl, M, N, e) || !source(a.res, f.res, f.rl, M, N, e))
+        return GBN_EINVAL;
+    if (M == 0) return GBN_OK;
+    const int sms = gbn::host_current_sms();
+    if (sms <= 0) return GBN_EDEVICE;
+    a.w = f.w;
+    a.s = f.s;
+    a.y = f.y;
+    a.q = f.q;
+    a.c = f.c;
+    a.rstd = f.rstd;
+    a.M = M;
+    a.N = (int)N;
+    a.eps = f.eps;
+    a.inv_n = (float)(1.0 / (double)N);
+    a.wt = f.wt;
+    a.variant = f.variant;
+    return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));
+}
+
+int norm_forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
+{
+    if (const int rc = norm_types(f.xt, f.wt, f.variant)) return rc;
+    if (!gbn::host_shape_ok(M, N) || !std::isfinite(f.eps) || f.eps < 0.f || !f.w)
+        return GBN_EINVAL;
+    if (!aligned(elem_bytes(f.wt), {f.w})) return GBN_EINVAL;
+    if (M > 0 && !f.x) return GBN_EINVAL;
+    if (f.s && !f.res && M > 0) return GBN_EINVAL;  // without res the stream is x
+    return forward(f, M, N, stream);
+}
+
+int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_t group, int ct,
+                  const void* dy, const gbn_rows* dyl, const void* ds, const gbn_rows* dsl,
+                  const void* w, const float* rstd, void* dx, void* dw, int64_t M, int64_t N,
+                  int xt, int wt, int variant, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (const int rc = norm_types(xt, wt, variant)) return rc;
+    if (!gbn::host_shape_ok(M, N) || !w) return GBN_EINVAL;
+    if (M > 0 && (!s || !dy || !dx || !rstd)) return GBN_EINVAL;
+    const int e = elem_bytes(xt), se = cscale ? 1 : e;
+    if (!aligned(se, {s}) || !aligned(e, {dy, ds, dx}) || !aligned(elem_bytes(wt), {w, dw}) ||
+        !aligned(4, {rstd, cscale}))
+        return GBN_EINVAL;
+    if (dw && ws && !aligned(4, {ws})) return GBN_EINVAL;
+    gbn::BwdArgs a{};
+    if (!source(a.s, s, sl, M, N, se) || !source(a.dy, dy, dyl, M, N, e) ||
+        !source(a.ds, ds, dsl, M, N, e))
+        return GBN_EINVAL;
+    const int sms = gbn::host_current_sms();
+    if (sms <= 0) return GBN_EDEVICE;
+    const int64_t P = M > 0 ? gbn::add_bwd_general_rows(M, N, sms) : 0;
+    if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
+        return GBN_EWORKSPACE;
+    if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
+    a.w = w;
+    a.rstd = rstd;
+    a.dx = dx;
+    a.ws = dw ? static_cast<float*>(ws) : nullptr;
+    a.M = M;
+    a.N = (int)N;
+    a.inv_n = (float)(1.0 / (double)N);
+    a.wt = wt;
+    a.variant = variant;
+    if (M > 0)
+        if (const int rc = launch_status(gbn::launch_add_bwd_general(stream, xt, P, a))) return rc;
+    if (!dw) return GBN_OK;
+    return launch_status(gbn::launch_colsum(stream, a.ws, P, N, N, wt, dw, nullptr, nullptr));
+}
+
+}  // namespace
+
+extern "C" {
+
+int rmsnorm_add_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                    const void* w, void* s, void* y, float* rstd, int64_t M, int64_t N, float eps,
+                    int xt, int wt, int variant, cudaStream_t stream)
+{
+    if (M > 0 && !y) return GBN_EINVAL;
+    return norm_forward({x, xl, res, rl, w, s, y, rstd, {}, {}, eps, xt, wt, variant}, M, N,
+                        stream);
+}
+
+int rmsnorm_add_quant_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                          const void* w, void* s, void* q, float* scale, float* rstd, int64_t M,
+                          int64_t N, int64_t group, float eps, int xt, int wt, int qt, int variant,
+                          cudaStream_t stream)
+{
+    if (!q8_ok(qt)) return GBN_EDTYPE;
+    if (!group_ok(group) || (M > 0 && (!q || !scale))) return GBN_EINVAL;
+    if (N < 1) return GBN_EINVAL;
+    return norm_forward({x, xl, res, rl, w, s, nullptr, rstd, q8_of(q, scale, qt, N, group), {},
+                         eps, xt, wt, variant},
+                        M, N, stream);
+}
+
+int rmsnorm_add_ckpt_fwd(const void* x, const gbn_rows* xl, const void* res, const gbn_rows* rl,
+                         const void* w, void* s, void* y, float* rstd, void* c, float* cscale,
+                         int64_t M, int64_t N, int64_t group, float eps, int xt, int wt, int ct,
+                         int variant, cudaStream_t stream)
+{
+    if (!q8_ok(ct)) return GBN_EDTYPE;
+    if (!group_ok(group) || (M > 0 && (!y || !c || !cscale))) return GBN_EINVAL;
+    if (N < 1) return GBN_EINVAL;
+    return norm_forward({x, xl, res, rl, w, s, y, rstd, {}, q8_of(c, cscale, ct, N, group), eps,
+                         xt, wt, variant},
+                        M, N, stream);
+}
+
+int rmsnorm_add_bwd(const void* s, const gbn_rows* sl, const void* dy, const gbn_rows* dyl,
+                    const void* ds, const gbn_rows* dsl, const void* w, const float* rstd,
+                    void* dx, void* dw, int64_t M, int64_t N, int xt, int wt, int variant,
+                    void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    return norm_backward(s, sl, nullptr, 0, GBN_E4M3, dy, dyl, ds, dsl, w, rstd, dx, dw, M, N, xt,
+                         wt, variant, ws, ws_bytes, stream);
+}
+
+int rmsnorm_add_ckpt_bwd(const void* c, const float* cscale, const void* dy, const gbn_rows* dyl,
+                         const void* ds, const gbn_rows* dsl, const void* w, const float* rstd,
+                         void* dx, void* dw, int64_t M, int64_t N, int64_t group, int xt, int wt,
+                         int ct, int variant, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!q8_ok(ct)) return GBN_EDTYPE;
+    if (!group_ok(group)) return GBN_EINVAL;
+    if (M > 0 && !cscale) return GBN_EINVAL;
+    return norm_backward(c, nullptr, cscale, group, ct, dy, dyl, ds, dsl, w, rstd, dx, dw, M, N,
+                         xt, wt, variant, ws, ws_bytes, stream);
+}
+
+int act_pack8(const void* x, const gbn_rows* xl, void* c, float* cscale, int64_t M, int64_t N,
+              int64_t group, int xt, int ct, cudaStream_t stream)
+{
+    if (!dtype_ok(xt) || !q8_ok(ct)) return GBN_EDTYPE;
+    if (!gbn::host_shape_ok(M, N) || !group_ok(group)) return GBN_EINVAL;
+    if (M > 0 && (!x || !c || !cscale)) return GBN_EINVAL;
+    return forward({x, xl, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, {},
+                    q8_of(c, cscale, ct, N, group), 0.f, xt, GBN_F32, GBN_RMS_WEIGHT_FIRST},
+                   M, N, stream);
+}
+
+int act_unpack8(const void* c, const float* cscale, void* x, int64_t M, int64_t N, int64_t group,
+                int xt, int ct, cudaStream_t stream)
+{
+    if (!dtype_ok(xt) || !q8_ok(ct)) return GBN_EDTYPE;
+    if (!gbn::host_shape_ok(M, N) || !group_ok(group)) return GBN_EINVAL;
+    if (M > 0 && (!x || !c || !cscale)) return GBN_EINVAL;
+    if (!aligned(elem_bytes(xt), {x}) || !aligned(4, {cscale})) return GBN_EINVAL;
+    if (M == 0) return GBN_OK;
+    const int sms = gbn::host_current_sms();
+    if (sms <= 0) return GBN_EDEVICE;
+    gbn::UnpackArgs a{};
+    a.c = q8_of(const_cast<void*>(c), cscale, ct, N, group);
+    a.x = x;
+    a.M = M;
+    a.N = (int)N;
+    return launch_status(gbn::launch_unpack_general(stream, xt, sms, a));
+}
+
+}  // extern "C"

@@ -391,6 +391,38 @@ bool layout_extent_ok(const gbn_rows& l, int64_t M, int64_t e)
     return t < (int64_t(1) << 62);
 }
 
+// One input's layout as a row map in bytes; false when it is not valid.
+// `scattered` says whether its rows are elsewhere than at r * N.
+bool layout_map(const gbn_rows* l, int64_t M, int64_t N, int64_t e, gbn::RowMap& m,
+                bool& scattered)
+{
+    m = gbn::RowMap{M > 0 ? M : 1, N * e, 1, 0, 0};
+    scattered = false;
+    if (!l) return true;
+    if (l->n1 < 1 || l->n2 < 1 || l->s1 < 0 || l->s2 < 0 || l->s3 < 0 ||
+        !layout_extent_ok(*l, M, e))
+        return false;
+    if (contiguous_rows(*l, M, N)) return true;
+    // Levels beyond the M rows change no row offset; capping them keeps
+    // n1 * n2 <= 2 M in the kernels' index arithmetic.
+    const int64_t n1 = l->n1 < M ? l->n1 : M;
+    const int64_t q = (M + n1 - 1) / n1;
+    const int64_t n2 = l->n2 < q ? l->n2 : q;
+    // The stride of a level that no row reaches multiplies only zero
+    // (n1 == 1: every r % n1 is 0; n2 == 1: every (r / n1) % n2 is 0;
+    // n1 * n2 >= M: every r / (n1 n2) is 0), so it is dropped before it
+    // is scaled to bytes: a huge unused stride must not overflow.  The
+    // strides that are reached were bounded by layout_extent_ok.
+    int64_t b1 = 0, b2 = 0, b3 = 0;
+    if ((n1 > 1 && __builtin_mul_overflow(l->s1, e, &b1)) ||
+        (n2 > 1 && __builtin_mul_overflow(l->s2, e, &b2)) ||
+        (n1 * n2 < M && __builtin_mul_overflow(l->s3, e, &b3)))
+        return false;
+    m = gbn::RowMap{n1, b1, n2, b2, b3};
+    scattered = true;
+    return true;
+}
+
 Inputs input_layouts(const gbn_rows* xl, const gbn_rows* dyl, const void* x, const void* dy,
                      int64_t M, int64_t N, int xt)
 {
@@ -402,33 +434,12 @@ Inputs input_layouts(const gbn_rows* xl, const gbn_rows* dyl, const void* x, con
     const void* base[2] = {x, dy};
     for (int t = 0; t < 2; ++t) {
         gbn::RowMap& m = in.maps.m[t];
-        m = gbn::RowMap{M > 0 ? M : 1, N * e, 1, 0, 0};
-        const gbn_rows* l = ls[t];
-        if (!l) continue;
-        if (l->n1 < 1 || l->n2 < 1 || l->s1 < 0 || l->s2 < 0 || l->s3 < 0 ||
-            !layout_extent_ok(*l, M, e)) {
+        bool scattered = false;
+        if (!layout_map(ls[t], M, N, e, m, scattered)) {
             in.ok = false;
             continue;
         }
-        if (contiguous_rows(*l, M, N)) continue;
-        // Levels beyond the M rows change no row offset; capping them keeps
-        // n1 * n2 <= 2 M in the kernels' index arithmetic.
-        const int64_t n1 = l->n1 < M ? l->n1 : M;
-        const int64_t q = (M + n1 - 1) / n1;
-        const int64_t n2 = l->n2 < q ? l->n2 : q;
-        // The stride of a level that no row reaches multiplies only zero
-        // (n1 == 1: every r % n1 is 0; n2 == 1: every (r / n1) % n2 is 0;
-        // n1 * n2 >= M: every r / (n1 n2) is 0), so it is dropped before it
-        // is scaled to bytes: a huge unused stride must not overflow.  The
-        // strides that are reached were bounded by layout_extent_ok.
-        int64_t b1 = 0, b2 = 0, b3 = 0;
-        if ((n1 > 1 && __builtin_mul_overflow(l->s1, e, &b1)) ||
-            (n2 > 1 && __builtin_mul_overflow(l->s2, e, &b2)) ||
-            (n1 * n2 < M && __builtin_mul_overflow(l->s3, e, &b3))) {
-            in.ok = false;
-            continue;
-        }
-        m = gbn::RowMap{n1, b1, n2, b2, b3};
+        if (!scattered) continue;
         in.scattered |= 1 << t;
         if (!aligned16(base[t]) || (m.s1 | m.s2 | m.s3) % 16 != 0) in.vec_ok = false;
     }
@@ -466,6 +477,20 @@ void prefer_batch(Launch& L, const Inputs& in, int64_t M, int64_t N, int xt, boo
 }
 
 }  // namespace
+
+namespace gbn {
+
+int host_sm_count(int device) { return sm_count(device); }
+int host_current_sms() { return current_sms(); }
+unsigned* host_fault_ptr() { return fault_ptr(); }
+bool host_shape_ok(int64_t M, int64_t N) { return shape_ok(M, N); }
+bool host_layout_map(const void* layout, int64_t M, int64_t N, int64_t e, RowMap& m,
+                     bool& scattered)
+{
+    return layout_map(static_cast<const gbn_rows*>(layout), M, N, e, m, scattered);
+}
+
+}  // namespace gbn
 
 extern "C" {
 
@@ -514,12 +539,13 @@ const char* gbn_status_string(int status)
 
 size_t gbn_bwd_workspace_bytes(int op, int64_t M, int64_t N, int xt, int pt, int device)
 {
-    if (op < GBN_OP_DYT || op > GBN_OP_RMSNORM || !shape_ok(M, N) || !dtype_ok(xt) ||
+    if (op < GBN_OP_DYT || op > GBN_OP_RMSNORM_ADD || !shape_ok(M, N) || !dtype_ok(xt) ||
         !dtype_ok(pt))
         return (size_t)-1;
     if (M == 0) return 0;
     const int sms = sm_count(device);
     if (sms <= 0) return (size_t)-1;
+    if (op == GBN_OP_RMSNORM_ADD) return gbn::add_bwd_workspace_bytes(M, N, xt, sms);
     const int kind =
         op == GBN_OP_DYT ? gbn::kBwdDyT : op == GBN_OP_LAYERNORM ? gbn::kBwdLN : gbn::kBwdRms;
     // the vector path with the kernel's wide set, or the general path

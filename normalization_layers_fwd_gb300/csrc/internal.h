@@ -61,6 +61,21 @@ struct Launch {
 // Host-side caches of device addresses and function attributes key on it.
 uint64_t current_ctx_id();
 
+// Host helpers of api.cu that the other dispatch files share: the SM count
+// of a device and of the current one (<= 0 when it cannot be queried), the
+// current device's fault word, the shape rule of every entry point, and one
+// input's gbn_rows layout (null: contiguous) as a row map in bytes.
+int host_sm_count(int device);
+int host_current_sms();
+unsigned* host_fault_ptr();
+bool host_shape_ok(int64_t M, int64_t N);
+bool host_layout_map(const void* layout, int64_t M, int64_t N, int64_t elem_bytes, RowMap& m,
+                     bool& scattered);
+
+// Workspace bytes of the residual-add backwards (add_api.cu), an upper bound
+// over their paths.
+size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms);
+
 // Workspace row length (floats) per layer: the per-column partial sums of
 // every parameter gradient, plus one scalar for DyT's alpha.
 inline int64_t ws_row_floats(int op, int64_t N)

@@ -23,9 +23,11 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libgbnorm.so")
 
-SOURCES = ["add_api.cu", "addnorm.cu", "api.cu", "colsum.cu", "dyt.cu", "layernorm.cu", "rmsnorm.cu", "rmsnorm_bwd.cu",
-           "static_ws.cu"]
-HEADERS = ["addnorm.cuh", "common.cuh", "ctx_cache.h", "internal.h", "rmsnorm.cuh"]
+SOURCES = ["add_api.cu", "addbwd_bf16.cu", "addbwd_f16.cu", "addbwd_f32.cu", "addfwd_bf16.cu",
+           "addfwd_f16.cu", "addfwd_f32.cu", "addnorm.cu", "api.cu", "colsum.cu", "dyt.cu",
+           "layernorm.cu", "rmsnorm.cu", "rmsnorm_bwd.cu", "static_ws.cu", "unpack8.cu"]
+HEADERS = ["addbwd.cuh", "addfwd.cuh", "addnorm.cuh", "common.cuh", "ctx_cache.h", "internal.h",
+           "rmsnorm.cuh", "rowring.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE,

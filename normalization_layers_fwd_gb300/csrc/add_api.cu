@@ -7,16 +7,7 @@
 #include "addnorm.cuh"
 #include "gbnorm.h"
 #include "internal.h"
-
-namespace gbn {
-
-size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int, int sms)
-{
-    const size_t need = (size_t)add_bwd_general_rows(M, N, sms) * (size_t)N * sizeof(float);
-    return (need + 255) & ~(size_t)255;
-}
-
-}  // namespace gbn
+#include "rowring.cuh"
 
 namespace {
 
@@ -70,6 +61,65 @@ gbn::Q8 q8_of(void* v, const float* scale, int type, int64_t N, int64_t group)
     return q;
 }
 
+// The fast kernels' schedule for rows of N elements: the first that holds a
+// row's vectors, one more than N / VEC where rows start inside a vector.
+int row_sched(int64_t N, int vec, bool edge)
+{
+    const int64_t nvec = edge ? (N + 2 * vec - 2) / vec : N / vec;
+    for (int s = 0; s < gbn::kNumRowSched; ++s)
+        if (nvec <= gbn::kRow[s].cap) return s;
+    return -1;
+}
+
+int64_t row_ctas(int sid, bool bwd, bool edge, int sms)
+{
+    const int64_t ctas =
+        (int64_t)sms * (bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge));
+    // rows that start inside a vector need CTAs to step by a multiple of VEC rows
+    return ctas >= 8 ? ctas / 8 * 8 : ctas;
+}
+
+// The ring kernel's launch, or false where the general kernel takes the call:
+// every tensor on a 16-byte boundary, scattered rows whole vectors on such
+// boundaries, and a schedule for the width.  groups: the scales per row that
+// the kernel finds (0: none).
+bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const RowSrc* in, int nt,
+               std::initializer_list<const void*> outs, int groups, int sms)
+{
+    const int vec = 16 / elem_bytes(xt);
+    p = gbn::RowPlan{};
+    p.edge = N % vec != 0;
+    if (!aligned(16, outs)) return false;
+    for (int t = 0; t < nt; ++t) {
+        if (!aligned(16, {in[t].p})) return false;
+        if (in[t].scattered &&
+            (p.edge || (in[t].map.s1 | in[t].map.s2 | in[t].map.s3) % 16 != 0))
+            return false;
+    }
+    p.sid = row_sched(N, vec, p.edge);
+    if (p.sid < 0) return false;
+    const gbn::RowSched& e = gbn::kRow[p.sid];
+    p.R = gbn::row_R(p.sid);
+    p.stages = bwd ? gbn::bwd_stages(p.sid) : gbn::fwd_stages(p.sid);
+    p.nblocks = (M + p.R - 1) / p.R;
+    const int64_t cap = row_ctas(p.sid, bwd, p.edge, sms);
+    p.grid = (int)(p.nblocks < cap ? p.nblocks : cap);
+    if (p.edge && p.nblocks > cap && cap * p.R % vec != 0) return false;
+    uint32_t at = 0;
+    for (int t = 0; t < nt; ++t) {
+        p.off[t] = at;
+        if (in[t].p) at += (uint32_t)(p.R * in[t].row_bytes + 32 + 127) / 128 * 128;
+    }
+    p.stage_bytes = at;
+    p.gm_off = 128 + p.stages * at;
+    p.smem = p.gm_off + (p.edge && groups > 1 ? 2 * (size_t)p.R * groups * sizeof(float) : 0);
+    if (bwd) {  // the CTA's column sums take the drained ring
+        const size_t cols = 128 + (size_t)e.T * e.KV * vec * sizeof(float);
+        p.smem = p.smem > cols ? p.smem : cols;
+    }
+    return p.smem <= (size_t)gbn::kMaxSmem;
+}
+
 int launch_status(cudaError_t e) { return e == cudaSuccess ? GBN_OK : GBN_ELAUNCH; }
 
 // Every forward: what is asked for is what is not null (w null: act_pack8).
@@ -92,7 +142,7 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     if (!aligned(e, {f.x, f.res, f.s, f.y}) || !aligned(4, {f.rstd, f.q.scale, f.c.scale}))
         return GBN_EINVAL;
     gbn::FwdArgs a{};
-    if (!source(a.x, f.x, f.xl, M, N, e) || !source(a.res, f.res, f.rl, M, N, e))
+    if (!source(a.in[0], f.x, f.xl, M, N, e) || !source(a.in[1], f.res, f.rl, M, N, e))
         return GBN_EINVAL;
     if (M == 0) return GBN_OK;
     const int sms = gbn::host_current_sms();
@@ -109,7 +159,15 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     a.inv_n = (float)(1.0 / (double)N);
     a.wt = f.wt;
     a.variant = f.variant;
-    return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));
+    gbn::RowPlan p;
+    const gbn::Q8& q8 = f.q.v ? f.q : f.c;
+    if (!plan_rows(p, false, f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))
+        return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));
+    if (!(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
+    const int mode = !f.w ? gbn::kModeC : f.q.v ? gbn::kModeQ : f.c.v ? gbn::kModeYC : gbn::kModeY;
+    return launch_status(f.xt == gbn::kF32   ? gbn::launch_add_fwd_f32(stream, mode, a, p)
+                         : f.xt == gbn::kF16 ? gbn::launch_add_fwd_f16(stream, mode, a, p)
+                                             : gbn::launch_add_fwd_bf16(stream, mode, a, p));
 }
 
 int norm_forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
@@ -137,12 +195,15 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
         return GBN_EINVAL;
     if (dw && ws && !aligned(4, {ws})) return GBN_EINVAL;
     gbn::BwdArgs a{};
-    if (!source(a.s, s, sl, M, N, se) || !source(a.dy, dy, dyl, M, N, e) ||
-        !source(a.ds, ds, dsl, M, N, e))
+    if (!source(a.in[0], s, sl, M, N, se) || !source(a.in[1], dy, dyl, M, N, e) ||
+        !source(a.in[2], ds, dsl, M, N, e))
         return GBN_EINVAL;
     const int sms = gbn::host_current_sms();
     if (sms <= 0) return GBN_EDEVICE;
-    const int64_t P = M > 0 ? gbn::add_bwd_general_rows(M, N, sms) : 0;
+    gbn::RowPlan p{};
+    const bool fast = M > 0 && plan_rows(p, true, xt, M, N, a.in, 3, {dx}, 0, sms);
+    if (fast && !(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
+    const int64_t P = M == 0 ? 0 : fast ? p.grid : gbn::add_bwd_general_rows(M, N, sms);
     if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
         return GBN_EWORKSPACE;
     if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
@@ -155,13 +216,40 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     a.inv_n = (float)(1.0 / (double)N);
     a.wt = wt;
     a.variant = variant;
-    if (M > 0)
-        if (const int rc = launch_status(gbn::launch_add_bwd_general(stream, xt, P, a))) return rc;
+    if (M > 0) {
+        const int mode = cscale                           ? gbn::kBwdC
+                         : variant == GBN_RMS_CAST_FIRST ? gbn::kBwdCast
+                                                         : gbn::kBwdS;
+        const cudaError_t rc = !fast               ? gbn::launch_add_bwd_general(stream, xt, P, a)
+                               : xt == gbn::kF32 ? gbn::launch_add_bwd_f32(stream, mode, a, p)
+                               : xt == gbn::kF16 ? gbn::launch_add_bwd_f16(stream, mode, a, p)
+                                                 : gbn::launch_add_bwd_bf16(stream, mode, a, p);
+        if (launch_status(rc) != GBN_OK) return GBN_ELAUNCH;
+    }
     if (!dw) return GBN_OK;
     return launch_status(gbn::launch_colsum(stream, a.ws, P, N, N, wt, dw, nullptr, nullptr));
 }
 
 }  // namespace
+
+namespace gbn {
+
+size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
+{
+    const int vec = 16 / elem_bytes(xt);
+    const bool edge = N % vec != 0;
+    const int sid = row_sched(N, vec, edge);
+    int64_t P = add_bwd_general_rows(M, N, sms);
+    if (sid >= 0) {
+        const int64_t blocks = (M + row_R(sid) - 1) / row_R(sid), cap = row_ctas(sid, true, edge, sms);
+        const int64_t grid = blocks < cap ? blocks : cap;
+        P = P > grid ? P : grid;
+    }
+    const size_t need = (size_t)P * (size_t)N * sizeof(float);
+    return (need + 255) & ~(size_t)255;
+}
+
+}  // namespace gbn
 
 extern "C" {
 
@@ -247,6 +335,8 @@ int act_unpack8(const void* c, const float* cscale, void* x, int64_t M, int64_t 
     a.x = x;
     a.M = M;
     a.N = (int)N;
+    if (aligned(16, {c, x}) && N < (1 << 30))  // its column arithmetic is 32-bit
+        return launch_status(gbn::launch_unpack_fast(stream, xt, sms, a));
     return launch_status(gbn::launch_unpack_general(stream, xt, sms, a));
 }
 

@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kGenThreads) add_fwd_general(FwdArgs a)
     const bool norm = a.w != nullptr;
     const int64_t step = (int64_t)gridDim.x * kGroups;
     for (int64_t r = blockIdx.x * (int64_t)kGroups + threadIdx.x / W; r < a.M; r += step) {
-        const TX* xr = src_row<TX>(a.x, r);
-        const TX* rr = a.res.p ? src_row<TX>(a.res, r) : nullptr;
+        const TX* xr = src_row<TX>(a.in[0], r);
+        const TX* rr = a.in[1].p ? src_row<TX>(a.in[1], r) : nullptr;
         TX* sr = a.s ? static_cast<TX*>(a.s) + r * N : nullptr;
         // s of a column: the first walk adds, the later ones read the stored
         // stream (x or res may be overwritten by it by then)
@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(kGenThreads) add_bwd_general(BwdArgs a)
     if (wrow)
         for (int c = l; c < N; c += W) wrow[c] = 0.f;
     for (int64_t r = gi; r < a.M; r += step) {
-        const TX* sr = packed ? nullptr : src_row<TX>(a.s, r);
-        const unsigned char* cr = packed ? a.s.p + r * N : nullptr;
-        const TX* dyr = src_row<TX>(a.dy, r);
-        const TX* dsr = a.ds.p ? src_row<TX>(a.ds, r) : nullptr;
+        const TX* sr = packed ? nullptr : src_row<TX>(a.in[0], r);
+        const unsigned char* cr = packed ? a.in[0].p + r * N : nullptr;
+        const TX* dyr = src_row<TX>(a.in[1], r);
+        const TX* dsr = a.in[2].p ? src_row<TX>(a.in[2], r) : nullptr;
         const float rs = a.rstd[r];
         auto xh_at = [&](int c) {
             if (!packed) return ldf(sr + c) * rs;

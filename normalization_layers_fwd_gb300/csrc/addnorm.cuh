@@ -38,7 +38,7 @@ struct Q8 {
 };
 
 struct FwdArgs {
-    RowSrc x, res;  // res.p null: none
+    RowSrc in[2];   // x, res (p null: none)
     const void* w;  // null in act_pack8
     void *s, *y;    // nullable
     Q8 q, c;        // v null: none
@@ -50,8 +50,8 @@ struct FwdArgs {
 };
 
 struct BwdArgs {
-    RowSrc s, dy, ds;  // s: the stream, or the checkpoint's bytes; ds.p null: none
-    Q8 c;              // the checkpoint's type, groups and scales (v null: s is the stream)
+    RowSrc in[3];  // the stream s or the checkpoint's bytes, dy, ds (p null: none)
+    Q8 c;          // the checkpoint's type, groups and scales (scale null: in[0] is the stream)
     const void* w;
     const float* rstd;
     void* dx;
@@ -68,6 +68,29 @@ struct UnpackArgs {
     int64_t M;
     int N;
 };
+
+// The launch of a fast kernel (addnorm_fast.cuh): persistent CTAs over row
+// blocks of R rows through a ring of `stages` stages, each holding one block
+// of every input at off[t].
+struct RowPlan {
+    int sid, edge, grid;
+    int64_t nblocks;
+    int R, stages;
+    uint32_t off[3], stage_bytes, gm_off;  // gm_off: the group maxima's place
+    size_t smem;
+    unsigned* fault;
+};
+
+// One instance set per activation type (addfwd_*.cu, addbwd_*.cu).
+enum FwdMode : int { kModeY = 0, kModeQ = 1, kModeYC = 2, kModeC = 3 };
+enum BwdMode : int { kBwdS = 0, kBwdCast = 1, kBwdC = 2 };
+cudaError_t launch_add_fwd_bf16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
+cudaError_t launch_add_fwd_f16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
+cudaError_t launch_add_fwd_f32(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
+cudaError_t launch_add_bwd_bf16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
+cudaError_t launch_add_bwd_f16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
+cudaError_t launch_add_bwd_f32(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
+cudaError_t launch_unpack_fast(cudaStream_t st, int xt, int sms, const UnpackArgs& a);
 
 // Launches of the general kernels (any width, alignment and layout).
 // Forward: everything FwdArgs asks for; with w null only the checkpoint.

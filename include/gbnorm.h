@@ -316,7 +316,7 @@ int rmsnorm_bwd_static_ws(const void* x, const void* dy, const void* w, const fl
  *     scale = max(a (1 / qmax), 2^-100),   q = round(v (1 / scale)),
  *   rounded to nearest even.  (The floor keeps 1 / scale finite: a group of
  *   zeros holds zeros.)  A group with a NaN or an infinity gets a scale of
- *   NaN or infinity, so that all of it reads back as NaN. */
+ *   NaN, so that all of it reads back as NaN. */
 typedef enum { GBN_E4M3 = 8, GBN_INT8 = 9 } gbn_q8;
 
 /* s, y, rstd as above. */

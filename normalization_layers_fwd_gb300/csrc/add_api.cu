@@ -61,20 +61,30 @@ gbn::Q8 q8_of(void* v, const float* scale, int type, int64_t N, int64_t group)
     return q;
 }
 
-// The fast kernels' schedule for rows of N elements: the first that holds a
-// row's vectors, one more than N / VEC where rows start inside a vector.
-int row_sched(int64_t N, int vec, bool edge)
+// The vectors a row of N elements may touch: one more than N / VEC where rows
+// start inside a vector; and the first schedule that holds them (-1: none).
+int64_t row_vectors(int64_t N, int vec, bool edge)
 {
-    const int64_t nvec = edge ? (N + 2 * vec - 2) / vec : N / vec;
+    return edge ? (N + 2 * vec - 2) / vec : N / vec;
+}
+int find_sched(bool bwd, int64_t nvec)
+{
     for (int s = 0; s < gbn::kNumRowSched; ++s)
-        if (nvec <= gbn::kRow[s].cap) return s;
+        if (nvec <= gbn::row_sched(bwd, s).cap) return s;
     return -1;
 }
 
-int64_t row_ctas(int sid, bool bwd, bool edge, int sms)
+// CTAs of T threads on the device: as many as the kernel's register budget
+// (a launch bound) and, in the launch, shared memory allow.
+int64_t row_ctas(int sid, bool bwd, bool edge, int T, size_t smem, int sms)
 {
-    const int64_t ctas =
-        (int64_t)sms * (bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge));
+    const int minb = bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge);
+    int64_t per = 65536 / (gbn::row_regs(gbn::row_sched(bwd, sid).T, minb) * T);
+    if (smem) {
+        const int64_t fit = 227 * 1024 / (int64_t)(smem + 4096);  // its static part too
+        per = per < fit ? per : fit;
+    }
+    const int64_t ctas = (per < 1 ? 1 : per) * sms;
     // rows that start inside a vector need CTAs to step by a multiple of VEC rows
     return ctas >= 8 ? ctas / 8 * 8 : ctas;
 }
@@ -96,15 +106,13 @@ bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const Ro
             (p.edge || (in[t].map.s1 | in[t].map.s2 | in[t].map.s3) % 16 != 0))
             return false;
     }
-    p.sid = row_sched(N, vec, p.edge);
+    const int64_t nvec = row_vectors(N, vec, p.edge);
+    p.sid = find_sched(bwd, nvec);
     if (p.sid < 0) return false;
-    const gbn::RowSched& e = gbn::kRow[p.sid];
-    p.R = gbn::row_R(p.sid);
+    const gbn::RowSched& e = gbn::row_sched(bwd, p.sid);
+    p.W = gbn::row_W(bwd, p.sid, nvec);
+    p.R = gbn::row_R(bwd, p.sid, p.edge);
     p.stages = bwd ? gbn::bwd_stages(p.sid) : gbn::fwd_stages(p.sid);
-    p.nblocks = (M + p.R - 1) / p.R;
-    const int64_t cap = row_ctas(p.sid, bwd, p.edge, sms);
-    p.grid = (int)(p.nblocks < cap ? p.nblocks : cap);
-    if (p.edge && p.nblocks > cap && cap * p.R % vec != 0) return false;
     uint32_t at = 0;
     for (int t = 0; t < nt; ++t) {
         p.off[t] = at;
@@ -114,9 +122,13 @@ bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const Ro
     p.gm_off = 128 + p.stages * at;
     p.smem = p.gm_off + (p.edge && groups > 1 ? 2 * (size_t)p.R * groups * sizeof(float) : 0);
     if (bwd) {  // the CTA's column sums take the drained ring
-        const size_t cols = 128 + (size_t)e.T * e.KV * vec * sizeof(float);
+        const size_t cols = 128 + (size_t)p.W * e.G * e.KV * vec * sizeof(float);
         p.smem = p.smem > cols ? p.smem : cols;
     }
+    p.nblocks = (M + p.R - 1) / p.R;
+    const int64_t cap = row_ctas(p.sid, bwd, p.edge, p.W * e.G, p.smem, sms);
+    p.grid = (int)(p.nblocks < cap ? p.nblocks : cap);
+    if (p.edge && p.nblocks > cap && cap * p.R % vec != 0) return false;
     return p.smem <= (size_t)gbn::kMaxSmem;
 }
 
@@ -238,10 +250,13 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
 {
     const int vec = 16 / elem_bytes(xt);
     const bool edge = N % vec != 0;
-    const int sid = row_sched(N, vec, edge);
+    const int64_t nvec = row_vectors(N, vec, edge);
+    const int sid = find_sched(true, nvec);
     int64_t P = add_bwd_general_rows(M, N, sms);
     if (sid >= 0) {
-        const int64_t blocks = (M + row_R(sid) - 1) / row_R(sid), cap = row_ctas(sid, true, edge, sms);
+        const int64_t R = row_R(true, sid, edge), blocks = (M + R - 1) / R;
+        const int T = row_W(true, sid, nvec) * row_sched(true, sid).G;
+        const int64_t cap = row_ctas(sid, true, edge, T, 0, sms);
         const int64_t grid = blocks < cap ? blocks : cap;
         P = P > grid ? P : grid;
     }

@@ -8,47 +8,47 @@
 namespace gbn {
 namespace {
 
-// VEC 8-bit codes as floats.
-template <int VEC>
-__device__ __forceinline__ void unpack_vec8(const uint32_t (&v)[VEC / 4], f2 (&o)[VEC / 2], int type)
-{
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-        o[2 * i] = q8_unpack2(v[i] & 0xffffu, type);
-        o[2 * i + 1] = q8_unpack2(v[i] >> 16, type);
-    }
-}
-
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRow[S].T, bwd_minb(S))
+__global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
     add_bwd_ring(const __grid_constant__ BwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int W = kRow[S].W, T = kRow[S].T, KV = kRow[S].KV, U = row_U(S), G = T / W;
+    constexpr int kW = kRowBwd[S].W, G = kRowBwd[S].G, KV = kRowBwd[S].KV;
+    constexpr int U = row_U(true, S, kEdge), R = G * U, kWarps = kRowBwd[S].T / G / 32;
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
-    constexpr bool kPacked = kMode == kBwdC, kCast = kMode == kBwdCast;
+    constexpr bool kPacked = kMode == kBwdC, kCast = kMode == kBwdCast, kLean = row_lean(S);
     // words of a thread's vector of s: activations, or 8-bit codes
-    constexpr int NS = kPacked ? VEC / 4 : 4, ES = kPacked ? 1 : E;
+    constexpr int NS = kPacked ? VEC / 4 : 4, VS = kPacked ? VEC : 16, ES = kPacked ? 1 : E;
+    constexpr int kRed = row_red_floats<kW, kWarps, G, U, false>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[row_red_floats<W, T, U, false>()];
+    __shared__ float red[kRed];
     int parity = 0;
-    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
+    const int N = a.N, W = kW ? kW : pl.W;
+    const int g = G == 1 ? 0 : threadIdx.x / W, l = threadIdx.x - g * W;
+    if constexpr (kW == 0) row_red_init<kRed>(red);
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
-    const int64_t first_row = (int64_t)blockIdx.x * pl.R + g;
-    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(first_row * N % VEC) : 0, N);
+
+    int64_t row = (int64_t)blockIdx.x * R + g;  // this thread's first row
+    const Cols<VEC, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P], acc[KV][P];
-    load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    load_weights<VEC, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
 #pragma unroll
     for (int j = 0; j < KV; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) acc[j][p] = splat2(0.f);
     // expression 0 with a weight of x's type rounds each term of dw
     const bool round_terms = kCast && a.wt == dtype_code<TX>();
+    int64_t at = row * N - cols.first + l * VEC;
+    const int64_t row_step = (int64_t)gridDim.x * R, at_step = row_step * N;
+    const uint32_t so0 = pl.off[0] + row_off(a.in[0], kPacked ? 0 : row - g, g) -
+                         cols.first * ES + l * VS;
+    const uint32_t so1 = pl.off[1] + row_off(a.in[1], row - g, g) - cols.first * E + l * 16;
+    const uint32_t so2 = pl.off[2] + row_off(a.in[2], row - g, g) - cols.first * E + l * 16;
 
     // A row's rstd, and the scales of its vectors' groups, are loaded one row
     // block ahead of their use.  kEdge: elements from eb on take the second.
     int ga[KV], eb[KV];
-    if constexpr (kPacked)
+    if constexpr (kPacked) {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
             const int c = cols.col(j) < 0 ? 0 : cols.col(j);
@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kRow[S].T, bwd_minb(S))
             ga[j] = whole ? 0 : c >> a.c.shift;
             eb[j] = kEdge && !whole ? ((ga[j] + 1) << a.c.shift) - cols.col(j) : VEC;
         }
+    }
     constexpr int kSc = kPacked ? (kEdge ? 2 : 1) : 0;
     float rs_n[U], sc_n[U][KV][kSc ? kSc : 1];
     auto load_stats = [&](int64_t row0) {
@@ -65,62 +66,78 @@ __global__ void __launch_bounds__(kRow[S].T, bwd_minb(S))
             const bool ok = r < a.M;
             rs_n[u] = ok ? __ldca(a.rstd + r) : 0.f;
             if constexpr (kPacked) {
+                const float* const scr = a.c.scale + r * a.c.ng;
 #pragma unroll
                 for (int j = 0; j < KV; ++j) {
-                    const float* sc = a.c.scale + r * a.c.ng + ga[j];
                     const bool in = ok && cols.ok(j);
-                    sc_n[u][j][0] = in ? __ldca(sc) : 0.f;
+                    sc_n[u][j][0] = in ? __ldca(scr + ga[j]) : 0.f;
                     if constexpr (kEdge)
                         sc_n[u][j][1] =
-                            in && eb[j] < VEC && ga[j] + 1 < a.c.ng ? __ldca(sc + 1) : 0.f;
+                            in && eb[j] < VEC && ga[j] + 1 < a.c.ng ? __ldca(scr + ga[j] + 1) : 0.f;
                 }
             }
         }
     };
-    load_stats(first_row);
+    load_stats(row);
 
     row_ring(a.in, pl, a.M, dsm, K, [&](int64_t b, const unsigned char* slot, bool alive) {
-        const int64_t r0 = b * pl.R;
         const bool last = b == pl.nblocks - 1;
-        uint32_t sp[U][KV][NS];
-        uint4 dyp[U][KV], dsp[U][KV];
         float rs[U], sc[U][KV][kSc ? kSc : 1], sum[U], none[U];
         bool okr[U];
+        // a block of 8-bit rows may start anywhere in a 16-byte unit
+        const uint32_t sc0 = kPacked ? ((uint32_t)(b * R) * (uint32_t)N) & 15u : 0u;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = g + u * G;
-            const int64_t r = r0 + i;
-            okr[u] = alive && r < a.M;
+            okr[u] = alive && (!last || row + u * G < a.M);
             rs[u] = rs_n[u];
-            const uint32_t o0 = row_off(a.in[0], r0, i) - cols.first * ES;
-            const uint32_t o1 = row_off(a.in[1], r0, i) - cols.first * E;
-            const uint32_t o2 = row_off(a.in[2], r0, i) - cols.first * E;
+            if constexpr (kPacked) {
 #pragma unroll
-            for (int j = 0; j < KV; ++j) {
-                const bool ok = okr[u] && cols.ok(j);
-                const int v = l + j * W;
-                const int64_t at = r * N - cols.first + (int64_t)v * VEC;
-                if constexpr (kPacked) {
-                    ld_vec8<VEC, kEdge>(sp[u][j], slot + pl.off[0], o0 + v * VEC, ok, a.in[0],
-                                        last, at, cols.em[j]);
+                for (int j = 0; j < KV; ++j)
 #pragma unroll
                     for (int q = 0; q < kSc; ++q) sc[u][j][q] = sc_n[u][j][q];
-                } else {
-                    const uint4 q = ld_vec<TX, kEdge>(slot + pl.off[0], o0 + v * 16, ok, a.in[0],
-                                                      last, at * E, cols.em[j]);
-                    sp[u][j][0] = q.x, sp[u][j][1] = q.y, sp[u][j][2] = q.z, sp[u][j][3] = q.w;
-                }
-                dyp[u][j] = ld_vec<TX, kEdge>(slot + pl.off[1], o1 + v * 16, ok, a.in[1], last,
-                                              at * E, cols.em[j]);
-                dsp[u][j] = ld_vec<TX, kEdge>(slot + pl.off[2], o2 + v * 16, ok && a.in[2].p,
-                                              a.in[2], last, at * E, cols.em[j]);
             }
         }
-        load_stats(r0 + (int64_t)gridDim.x * pl.R + g);
-        // xhat and dn of one vector
-        auto terms = [&](int u, int j, f2 (&xh)[P], f2 (&dn)[P], f2 (&dv)[P]) {
+        auto ld_s = [&](int u, int j, uint32_t (&v)[NS]) {
+            const bool ok = okr[u] && cols.ok(j);
+            const int64_t e = at + (int64_t)u * G * N + j * W * VEC;
+            const uint32_t o = so0 + u * G * (uint32_t)a.in[0].row_bytes + j * W * VS;
             if constexpr (kPacked) {
-                unpack_vec8<VEC>(sp[u][j], xh, a.c.type);
+                ld_vec8<VEC, kEdge>(v, slot, sc0 + o, ok, a.in[0], last, e, cols.em[j]);
+            } else {
+                const uint4 q =
+                    ld_vec<TX, kEdge>(slot, o, ok, a.in[0], last, e * E, cols.em[j]);
+                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+            }
+        };
+        auto ld_act = [&](int u, int j, int t, uint32_t so) {
+            const bool ok = okr[u] && cols.ok(j) && (t == 1 || a.in[2].p);
+            const int64_t e = at + (int64_t)u * G * N + j * W * VEC;
+            const uint32_t o = so + u * G * (uint32_t)a.in[1].row_bytes + j * W * 16;
+            return ld_vec<TX, kEdge>(slot, o, ok, a.in[t], last, e * E, cols.em[j]);
+        };
+        uint32_t sp[U][KV][NS];
+        uint4 dyp[U][KV], dsp[U][KV];
+        if constexpr (!kLean) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < KV; ++j) {
+                    ld_s(u, j, sp[u][j]);
+                    dyp[u][j] = ld_act(u, j, 1, so1);
+                    dsp[u][j] = ld_act(u, j, 2, so2);
+                }
+        }
+        load_stats(row + row_step);
+        // xhat, dn and dy of one vector
+        auto terms = [&](int u, int j, f2 (&xh)[P], f2 (&dn)[P], f2 (&dv)[P]) {
+            if constexpr (kLean) {
+                ld_s(u, j, sp[u][j]);
+                dyp[u][j] = ld_act(u, j, 1, so1);
+            }
+            if constexpr (kPacked) {
+#pragma unroll
+                for (int i = 0; i < VEC / 4; ++i)
+                    q8_unpack4(sp[u][j][i], xh[2 * i], xh[2 * i + 1], a.c.type);
                 const float ka = sc[u][j][0] * rs[u];
                 if constexpr (kEdge) {
                     const float kb = sc[u][j][kSc - 1] * rs[u];
@@ -167,31 +184,33 @@ __global__ void __launch_bounds__(kRow[S].T, bwd_minb(S))
             }
             sum[u] = lo2(q) + hi2(q);
         }
-        row_reduce<W, T, U, false>(sum, none, red, parity);
+        row_reduce<kW, kWarps, G, U, false>(sum, none, red, parity, g, l);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = r0 + g + u * G;
             const f2 r2 = splat2(rs[u]), nm = splat2(-(sum[u] * a.inv_n));
-            TX* const dxr = static_cast<TX*>(a.dx) + (r * N - cols.first);
+            TX* const dxr = static_cast<TX*>(a.dx) + at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
                 f2 xh[P], dn[P], dv[P];
                 terms(u, j, xh, dn, dv);
+                if constexpr (kLean) dsp[u][j] = ld_act(u, j, 2, so2);
                 unpack2<TX>(dsp[u][j], dv);
 #pragma unroll
                 for (int p = 0; p < P; ++p) dv[p] = fma2(r2, fma2(xh[p], nm, dn[p]), dv[p]);
-                st_vec<TX, kEdge>(dxr + (l + j * W) * VEC, pack2<TX>(dv), okr[u] && cols.ok(j),
+                st_vec<TX, kEdge>(dxr + j * W * VEC, pack2<TX>(dv), okr[u] && cols.ok(j),
                                   cols.em[j]);
             }
         }
-        return W > 32;  // row_reduce's barrier came after the last slot read
+        row += row_step;
+        at += at_step;
+        return kW == 0 && !kLean;  // row_reduce's barrier came after the last slot read
     });
 
     if (a.ws == nullptr) return;  // no weight gradient wanted (uniform)
     // The CTA's column sums, its row groups added in order: each group leaves
     // its vectors in the drained ring, and column c of group q is found
     // `first` of that group's rows further on.
-    constexpr int kCap = W * KV * VEC;
+    const int cap = W * KV * VEC;
     float* const out = a.ws + blockIdx.x * (int64_t)N;
     if constexpr (G == 1) {
 #pragma unroll
@@ -208,16 +227,15 @@ __global__ void __launch_bounds__(kRow[S].T, bwd_minb(S))
         for (int j = 0; j < KV; ++j)
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                *reinterpret_cast<float2*>(buf + g * kCap + (l + j * W) * VEC + 2 * p) =
+                *reinterpret_cast<float2*>(buf + g * cap + cols.vec(j) * VEC + 2 * p) =
                     make_float2(lo2(acc[j][p]), hi2(acc[j][p]));
         __syncthreads();
-        for (int c = threadIdx.x; c < N; c += T) {
+        for (int c = threadIdx.x; c < N; c += blockDim.x) {
             float t = 0.f;
 #pragma unroll 4
             for (int q = 0; q < G; ++q) {
-                const int first =
-                    kEdge ? (int)(((int64_t)blockIdx.x * pl.R + q) * N % VEC) : 0;
-                t += buf[q * kCap + c + first];
+                const int first = kEdge ? (int)(((int64_t)blockIdx.x * R + q) * N % VEC) : 0;
+                t += buf[q * cap + c + first];
             }
             out[c] = t;
         }
@@ -231,7 +249,7 @@ cudaError_t bwd_launch(cudaStream_t st, int mode, const BwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_bwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, kRow[S].T, p.smem, st, a, p);
+        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * kRowBwd[S].G, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -12,43 +12,51 @@ namespace gbn {
 namespace {
 
 // VEC values times k (ka before element eb, kb from it on) as 8-bit codes.
-template <int VEC>
+template <int VEC, bool kTwo>
 __device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v)[VEC / 2],
                                           float ka, float kb, int eb, int type)
 {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
-        uint32_t h[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int p = 2 * i + q;
-            h[q] = q8_pack2(lo2(v[p]) * (2 * p < eb ? ka : kb),
-                            hi2(v[p]) * (2 * p + 1 < eb ? ka : kb), type);
+        f2 k0 = splat2(ka), k1 = k0;
+        if constexpr (kTwo) {
+            k0 = mk2(4 * i < eb ? ka : kb, 4 * i + 1 < eb ? ka : kb);
+            k1 = mk2(4 * i + 2 < eb ? ka : kb, 4 * i + 3 < eb ? ka : kb);
         }
-        out[i] = h[0] | (h[1] << 16);
+        out[i] = q8_pack4(v[2 * i], v[2 * i + 1], k0, k1, type);
     }
 }
 
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
+__global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
     add_fwd_ring(const __grid_constant__ FwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int W = kRow[S].W, T = kRow[S].T, KV = kRow[S].KV, U = row_U(S), G = T / W;
-    constexpr int VEC = Vec<TX>::kN, P = VEC / 2;
+    constexpr int kW = kRowFwd[S].W, G = kRowFwd[S].G, KV = kRowFwd[S].KV;
+    constexpr int U = row_U(false, S, kEdge), R = G * U, kWarps = kRowFwd[S].T / G / 32;
+    constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
     constexpr bool kNorm = kMode != kModeC, kMax = kMode != kModeY;
-    constexpr int E = (int)sizeof(TX);
+    constexpr int kRed = row_red_floats<kW, kWarps, G, U, kMax>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[row_red_floats<W, T, U, kMax>()];
+    __shared__ float red[kRed];
     int parity = 0;
-    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
+    const int N = a.N, W = kW ? kW : pl.W;
+    const int g = G == 1 ? 0 : threadIdx.x / W, l = threadIdx.x - g * W;
+    if constexpr (kW == 0) row_red_init<kRed>(red);
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
 
     // the first row of this thread; its later ones are a multiple of VEC rows on
-    const int64_t first_row = (int64_t)blockIdx.x * pl.R + g;
-    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(first_row * N % VEC) : 0, N);
+    int64_t row = (int64_t)blockIdx.x * R + g;
+    const Cols<VEC, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P];
-    if constexpr (kNorm) load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    if constexpr (kNorm) load_weights<VEC, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    // this thread's first vector: its element in the [M, N] tensors, and its
+    // byte in a slot (rows of a slot are row_bytes apart)
+    int64_t at = row * N - cols.first + l * VEC;
+    const int64_t row_step = (int64_t)gridDim.x * R, at_step = row_step * N;
+    const uint32_t so0 = pl.off[0] + row_off(a.in[0], row - g, g) - cols.first * E + l * 16;
+    const uint32_t so1 = pl.off[1] + row_off(a.in[1], row - g, g) - cols.first * E + l * 16;
+    const uint32_t srow = (uint32_t)G * (uint32_t)a.in[0].row_bytes;
 
     // 8-bit groups: the output's or the checkpoint's
     const Q8& q8 = kMode == kModeQ ? a.q : a.c;
@@ -56,6 +64,7 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
     const int lanes = whole ? W : (1 << q8.shift) / VEC;  // of a group, when rows are whole vectors
     // kEdge: a vector's elements before eb belong to group ga, the others to the next
     int ga[KV], eb[KV];
+    bool lead[KV];  // the vector holds its group's first column
     float* const gm = reinterpret_cast<float*>(dsm + pl.gm_off);  // [2][R][ng] maxima (kEdge)
     const bool shared_max = kEdge && kMax && !whole;
     if constexpr (kMax) {
@@ -64,48 +73,43 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
             const int c = cols.col(j) < 0 ? 0 : cols.col(j);
             ga[j] = whole ? 0 : c >> q8.shift;
             eb[j] = kEdge && !whole ? ((ga[j] + 1) << q8.shift) - cols.col(j) : VEC;
+            lead[j] = cols.ok(j) && (c & (whole ? -1 : (1 << q8.shift) - 1)) == 0;
         }
         if (shared_max) {
-            for (int i = threadIdx.x; i < 2 * pl.R * q8.ng; i += T) gm[i] = 0.f;
+            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += blockDim.x) gm[i] = 0.f;
             __syncthreads();
         }
     }
     int half = 0;  // of gm
 
     row_ring(a.in, pl, a.M, dsm, K, [&](int64_t b, const unsigned char* slot, bool alive) {
-        const int64_t r0 = b * pl.R;
         const bool last = b == pl.nblocks - 1;
         uint4 sp[U][KV];
         float ss[U], mx[U], gmx[U][KV];
         bool okr[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = g + u * G;
-            const int64_t r = r0 + i;
-            okr[u] = alive && r < a.M;
+            okr[u] = alive && (!last || row + u * G < a.M);
             ss[u] = 0.f;
             mx[u] = 0.f;
-            const uint32_t o0 = row_off(a.in[0], r0, i) - cols.first * E;
-            const uint32_t o1 = row_off(a.in[1], r0, i) - cols.first * E;
-            TX* const sr = static_cast<TX*>(a.s) + (r * N - cols.first);
+            TX* const sr = static_cast<TX*>(a.s) + at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
                 const bool ok = okr[u] && cols.ok(j);
-                const int v = l + j * W;  // the vector's place in the row
-                const int64_t gb = (r * N - cols.first + (int64_t)v * VEC) * E;
-                sp[u][j] = ld_vec<TX, kEdge>(slot + pl.off[0], o0 + v * 16, ok, a.in[0], last, gb,
-                                             cols.em[j]);
+                const uint32_t o = u * srow + j * W * 16;
+                const int64_t gb = (at + (int64_t)u * G * N + j * W * VEC) * E;
+                sp[u][j] = ld_vec<TX, kEdge>(slot, so0 + o, ok, a.in[0], last, gb, cols.em[j]);
                 if (a.in[1].p) {
-                    const uint4 rv = ld_vec<TX, kEdge>(slot + pl.off[1], o1 + v * 16, ok, a.in[1],
-                                                       last, gb, cols.em[j]);
+                    const uint4 rv =
+                        ld_vec<TX, kEdge>(slot, so1 + o, ok, a.in[1], last, gb, cols.em[j]);
                     f2 xa[P], xb[P];
                     unpack2<TX>(sp[u][j], xa);
                     unpack2<TX>(rv, xb);
 #pragma unroll
                     for (int p = 0; p < P; ++p) xa[p] = add2(xa[p], xb[p]);
                     sp[u][j] = pack2<TX>(xa);  // the stream, rounded once
+                    if (a.s) st_vec<TX, kEdge>(sr + j * W * VEC, sp[u][j], ok, cols.em[j]);
                 }
-                if (a.s) st_vec<TX, kEdge>(sr + v * VEC, sp[u][j], ok, cols.em[j]);
                 f2 sv[P];
                 unpack2<TX>(sp[u][j], sv);
                 if constexpr (kNorm) {
@@ -115,14 +119,19 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
                     ss[u] += lo2(q) + hi2(q);
                 }
                 if constexpr (kMax) {
-                    if constexpr (kMode == kModeQ)
+                    if constexpr (kMode == kModeQ) {
 #pragma unroll
                         for (int p = 0; p < P; ++p) sv[p] = mul2(sv[p], wf[j][p]);
+                    }
                     if (!shared_max) {
                         float m = 0.f;
+                        if constexpr (kMode == kModeQ) {
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            m = max_nan(max_nan(m, fabsf(lo2(sv[p]))), fabsf(hi2(sv[p])));
+                            for (int p = 0; p < P; ++p)
+                                m = max_nan(max_nan(m, fabsf(lo2(sv[p]))), fabsf(hi2(sv[p])));
+                        } else {
+                            m = vec_amax<TX>(sp[u][j]);
+                        }
                         gmx[u][j] = m;
                         mx[u] = max_nan(mx[u], m);
                     } else if (ok) {
@@ -134,7 +143,8 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
                             if (2 * p < eb[j]) ma = max_nan(ma, lo); else mb = max_nan(mb, lo);
                             if (2 * p + 1 < eb[j]) ma = max_nan(ma, hi); else mb = max_nan(mb, hi);
                         }
-                        int* const m = reinterpret_cast<int*>(gm) + (half * pl.R + i) * q8.ng + ga[j];
+                        int* const m = reinterpret_cast<int*>(gm) +
+                                       (half * R + g + u * G) * q8.ng + ga[j];
                         atomicMax(m, __float_as_int(ma));
                         if (eb[j] < VEC && ga[j] + 1 < q8.ng) atomicMax(m + 1, __float_as_int(mb));
                     }
@@ -143,11 +153,7 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
         }
         // the row's sum, and its maximum for a scale per row; a group's
         // maximum from its lanes, or from shared memory
-        if constexpr (kNorm) {
-            row_reduce<W, T, U, kMax>(ss, mx, red, parity);
-        } else if (whole) {
-            row_reduce<W, T, U, kMax>(ss, mx, red, parity);
-        }
+        if (kNorm || whole) row_reduce<kW, kWarps, G, U, kMax>(ss, mx, red, parity, g, l);
         if constexpr (kMax) {
             if (shared_max) {
                 __syncthreads();
@@ -163,16 +169,14 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = g + u * G;
-            const int64_t r = r0 + i;
+            const int64_t r = row + u * G;
             const float rs = kNorm ? rsqrtf(fmaf(ss[u], a.inv_n, a.eps)) : 1.f;
             const f2 r2 = splat2(rs);
             if (kNorm && a.rstd) st_f32_if(l == 0 && okr[u], a.rstd + r, rs);
-            const int64_t at = r * N - cols.first;  // of the row's first vector
+            const int64_t atu = at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
                 const bool ok = okr[u] && cols.ok(j);
-                const int v = l + j * W;
                 f2 sv[P];
                 unpack2<TX>(sp[u][j], sv);
                 if constexpr (kMode == kModeY || kMode == kModeYC) {
@@ -185,19 +189,20 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
 #pragma unroll
                         for (int p = 0; p < P; ++p) o[p] = mul2(wf[j][p], mul2(sv[p], r2));
                     }
-                    st_vec<TX, kEdge>(static_cast<TX*>(a.y) + at + v * VEC, pack2<TX>(o), ok,
+                    st_vec<TX, kEdge>(static_cast<TX*>(a.y) + atu + j * W * VEC, pack2<TX>(o), ok,
                                       cols.em[j]);
                 }
                 if constexpr (kMax) {
                     float ma = whole ? mx[u] : gmx[u][j], mb = 0.f;
                     if (shared_max && ok) {
-                        const float* m = gm + (half * pl.R + i) * q8.ng + ga[j];
+                        const float* m = gm + (half * R + g + u * G) * q8.ng + ga[j];
                         ma = m[0];
                         mb = eb[j] < VEC && ga[j] + 1 < q8.ng ? m[1] : 0.f;
                     }
-                    if constexpr (kMode == kModeQ)
+                    if constexpr (kMode == kModeQ) {
 #pragma unroll
                         for (int p = 0; p < P; ++p) sv[p] = mul2(sv[p], wf[j][p]);
+                    }
                     const float t = kMode == kModeQ ? rs : 1.f;  // r enters here
                     const float sa = q8_scale(ma * t, q8.type);
                     const float ka = t * __frcp_rn(sa);
@@ -207,25 +212,25 @@ __global__ void __launch_bounds__(kRow[S].T, fwd_minb(S, kEdge))
                         kb = t * __frcp_rn(sb);
                     }
                     uint32_t o[VEC / 4];
-                    pack_vec8<VEC>(o, sv, ka, kb, kEdge ? eb[j] : VEC, q8.type);
-                    st_vec8<VEC, kEdge>(static_cast<unsigned char*>(q8.v) + at + v * VEC, o, ok,
-                                        cols.em[j]);
+                    pack_vec8<VEC, kEdge>(o, sv, ka, kb, eb[j], q8.type);
+                    st_vec8<VEC, kEdge>(static_cast<unsigned char*>(q8.v) + atu + j * W * VEC, o,
+                                        ok, cols.em[j]);
                     // the vector that holds a group's first column writes its scale
                     float* const sc = q8.scale + r * q8.ng + ga[j];
-                    const int c = cols.col(j);
-                    const int mask = whole ? -1 : (1 << q8.shift) - 1;
-                    if (ok && ((c < 0 ? 0 : c) & mask) == 0) sc[0] = sa;
+                    if (okr[u] && lead[j]) sc[0] = sa;
                     if (shared_max && ok && eb[j] < VEC && ga[j] + 1 < q8.ng) sc[1] = sb;
                 }
             }
         }
+        row += row_step;
+        at += at_step;
         if (shared_max) {
             // the other half is free: its readers passed the barrier above
             half ^= 1;
-            for (int i = threadIdx.x; i < pl.R * q8.ng; i += T) gm[half * pl.R * q8.ng + i] = 0.f;
+            for (int i = threadIdx.x; i < R * q8.ng; i += blockDim.x) gm[half * R * q8.ng + i] = 0.f;
             return false;  // and a barrier before its next use
         }
-        return W > 32 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
+        return kW == 0 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
     });
 }
 
@@ -236,7 +241,7 @@ cudaError_t fwd_launch(cudaStream_t st, int mode, const FwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_fwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, kRow[S].T, p.smem, st, a, p);
+        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * kRowFwd[S].G, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kGenThreads) add_fwd_general(FwdArgs a)
                 const float k = out8 ? rs * __frcp_rn(sc) : __frcp_rn(sc);
                 if ((whole ? l : lane) == 0) row_q.scale[r * row_q.ng + g] = sc;
                 for (int c = (int)c0 + (whole ? l : lane); c < c1; c += whole ? W : 32)
-                    qr[c] = (unsigned char)q8_pack2(p_at(c, out8) * k, 0.f, row_q.type);
+                    qr[c] = (unsigned char)q8_pack1(p_at(c, out8), k, row_q.type);
             }
         }
     }
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kGenThreads) add_bwd_general(BwdArgs a)
         auto xh_at = [&](int c) {
             if (!packed) return ldf(sr + c) * rs;
             const float sc = a.c.scale[r * a.c.ng + (c >> a.c.shift)];
-            return lo2(q8_unpack2(cr[c], a.c.type)) * (sc * rs);
+            return q8_unpack1(cr[c], a.c.type) * (sc * rs);
         };
         auto dn_at = [&](int c) {
             const float v = ldf(dyr + c) * weight_at(a.w, a.wt, c, a.variant);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kGenThreads) unpack_general(UnpackArgs a)
         const int64_t r = i / a.N;
         const int c = (int)(i - r * a.N);
         const float sc = a.c.scale[r * a.c.ng + (c >> a.c.shift)];
-        x[i] = cast_x<TX>(lo2(q8_unpack2(q[i], a.c.type)) * sc);
+        x[i] = cast_x<TX>(q8_unpack1(q[i], a.c.type) * sc);
     }
 }
 

@@ -73,7 +73,7 @@ struct UnpackArgs {
 // blocks of R rows through a ring of `stages` stages, each holding one block
 // of every input at off[t].
 struct RowPlan {
-    int sid, edge, grid;
+    int sid, edge, grid, W;
     int64_t nblocks;
     int R, stages;
     uint32_t off[3], stage_bytes, gm_off;  // gm_off: the group maxima's place
@@ -109,36 +109,76 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// The scale of a group whose largest magnitude is a.
+// The scale of a group whose largest magnitude is a: NaN for an infinity or a
+// NaN (a - a), so that whatever the group's codes are they read back as NaN.
 __device__ __forceinline__ float q8_scale(float a, int type)
 {
-    return max_nan(a * q8_rmax(type), kScaleFloor);
+    return max_nan(fmaf(a, q8_rmax(type), a - a), kScaleFloor);
 }
 
-// Two values, already divided by their scale, as 8-bit codes (lo in the low
-// byte), rounded to nearest even.  A value exceeds qmax by at most the two
-// roundings of scale and 1 / scale, far less than half a step, so neither
-// type clips a finite value.
-__device__ __forceinline__ uint32_t q8_pack2(float lo, float hi, int type)
+// 8-bit codes of four values v times k (one over their scale; r entering with
+// it for an output), the first in the low byte, rounded to nearest even.  A
+// product exceeds qmax by at most the roundings of scale and 1 / scale, far
+// less than half a step, so neither type clips a finite value.  int8: adding
+// 1.5 2^23 leaves the nearest integer in the low bits of the sum (the spacing
+// of floats there is 1); the product is rounded before it, in instructions
+// that may not be fused (ptxas 13.0 did fuse mul.rn.f32x2 with
+// add.rn.f32x2, and products next to a half went the other way).
+__device__ __forceinline__ uint32_t q8_pack4(f2 a, f2 b, f2 ka, f2 kb, int type)
 {
     if (type == kE4M3) {
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+        a = mul2(a, ka);
+        b = mul2(b, kb);
+        uint32_t r;
+        asm("{\n\t.reg .b16 l, h;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+            "mov.b32 %0, {l, h};\n\t}"
+            : "=r"(r)
+            : "f"(lo2(a)), "f"(hi2(a)), "f"(lo2(b)), "f"(hi2(b)));
         return r;
     }
-    const int a = __float2int_rn(lo), b = __float2int_rn(hi);
-    return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8);
+    auto code = [](float v, float k) {
+        return __float_as_uint(__fadd_rn(__fmul_rn(v, k), 12582912.f));
+    };
+    return __byte_perm(__byte_perm(code(lo2(a), lo2(ka)), code(hi2(a), hi2(ka)), 0x0040),
+                       __byte_perm(code(lo2(b), lo2(kb)), code(hi2(b), hi2(kb)), 0x0040), 0x5410);
 }
 
-// Two 8-bit codes as floats (exact: e4m3 values are f16 values).
-__device__ __forceinline__ f2 q8_unpack2(uint32_t w, int type)
+// Four 8-bit codes as floats, exactly.  e4m3 values are f16 values.  int8: a
+// byte with its sign bit turned, under the exponent of 2^23, is 2^23 + 128 +
+// its value.
+__device__ __forceinline__ void q8_unpack4(uint32_t w, f2& a, f2& b, int type)
 {
     if (type == kE4M3) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
-        return h2_to_f2(h);
+        uint32_t l, h;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(l), "=r"(h)
+            : "r"(w));
+        a = h2_to_f2(l);
+        b = h2_to_f2(h);
+        return;
     }
-    return mk2((float)(int8_t)(w & 0xff), (float)(int8_t)((w >> 8) & 0xff));
+    const uint32_t t = w ^ 0x80808080u, e = 0x4b000000u;
+    const f2 m = splat2(-8388736.f);  // -(2^23 + 128)
+    a = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7440)),
+                 __uint_as_float(__byte_perm(t, e, 0x7441))), m);
+    b = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7442)),
+                 __uint_as_float(__byte_perm(t, e, 0x7443))), m);
+}
+
+// One value (the general kernels).
+__device__ __forceinline__ uint32_t q8_pack1(float v, float k, int type)
+{
+    return q8_pack4(mk2(v, 0.f), splat2(0.f), splat2(k), splat2(0.f), type) & 0xffu;
+}
+__device__ __forceinline__ float q8_unpack1(uint32_t b, int type)
+{
+    f2 v, unused;
+    q8_unpack4(b, v, unused, type);
+    return lo2(v);
 }
 
 }  // namespace gbn

@@ -23,32 +23,81 @@
 
 namespace gbn {
 
-// Row groups: rows of up to `cap` vectors go to W threads with KV vectors
-// each, of CTAs of T threads.  One vector a thread up to a warp's 32, then
-// two: half the warps, and half the reduction, that one would take.
+// Schedules.  A row of nvec vectors goes to a row group of W threads with KV
+// vectors each (vector v of the row to thread v % W); a CTA has G groups.  Up
+// to 64 vectors a group is (part of) a warp, with W the next power of two;
+// wider rows take as many warps as they fill, W = 32 ceil(nvec / (32 KV)), so
+// that no more than a warp's worth of lanes idles.  Two vectors a thread
+// halve the reduction that one would take.  The widest backward holds its
+// column sums and weights in registers (T <= 512 leaves 128 each) and reads
+// its row from the ring once more instead of keeping it (row_lean).
 struct RowSched {
-    int cap, W, T, KV;
+    int cap, W, G, KV, T;  // W 0: as many warps as the row fills, T / G threads at most
 };
 constexpr int kNumRowSched = 10;
-constexpr RowSched kRow[kNumRowSched] = {
-    {4, 4, 256, 1},    {8, 8, 256, 1},     {16, 16, 256, 1},   {32, 32, 256, 1},
-    {64, 32, 256, 2},  {128, 64, 256, 2},  {256, 128, 256, 2}, {512, 256, 256, 2},
-    {1024, 512, 512, 2}, {2048, 1024, 1024, 2},
+constexpr RowSched kRowFwd[kNumRowSched] = {
+    {4, 4, 64, 1, 256},    {8, 8, 32, 1, 256},   {16, 16, 16, 1, 256}, {32, 32, 8, 1, 256},
+    {64, 32, 8, 2, 256},   {128, 0, 4, 2, 256},  {256, 0, 2, 2, 256},  {512, 0, 1, 2, 256},
+    {1024, 0, 1, 2, 512},  {2048, 0, 1, 2, 1024},
 };
-// Rows a thread takes of a block, CTAs an SM, ring stages.
-constexpr int row_U(int S) { return kRow[S].KV == 1 ? 2 : 1; }
-constexpr int row_R(int S) { return kRow[S].T / kRow[S].W * row_U(S); }
+constexpr RowSched kRowBwd[kNumRowSched] = {
+    {4, 4, 64, 1, 256},    {8, 8, 32, 1, 256},   {16, 16, 16, 1, 256}, {32, 32, 8, 1, 256},
+    {64, 32, 8, 2, 256},   {128, 0, 4, 2, 256},  {256, 0, 2, 2, 256},  {512, 0, 1, 2, 256},
+    {1024, 0, 1, 2, 512},  {2048, 0, 1, 4, 512},
+};
+constexpr const RowSched& row_sched(bool bwd, int S) { return bwd ? kRowBwd[S] : kRowFwd[S]; }
+constexpr int row_W(bool bwd, int S, int64_t nvec)
+{
+    const RowSched& e = row_sched(bwd, S);
+    return e.W ? e.W : (int)((nvec + 32 * e.KV - 1) / (32 * e.KV)) * 32;
+}
+constexpr bool row_lean(int S) { return S == 9; }
+#ifndef GBN_FU
+#define GBN_FU 1
+#endif
+#ifndef GBN_BU
+#define GBN_BU 1
+#endif
+// Rows a thread takes of a block.  Rows that start inside a vector keep one
+// mask and one set of weights a thread, so a thread's rows of a block are a
+// multiple of VEC rows apart (G) or one.
+constexpr int row_U(bool bwd, int S, bool edge)
+{
+    const RowSched& e = row_sched(bwd, S);
+    return e.KV == 1 ? 2 : e.T > 512 || e.KV > 2 || (edge && e.G % 8 != 0) ? 1
+           : bwd ? GBN_BU : GBN_FU;
+}
+constexpr int row_R(bool bwd, int S, bool edge)
+{
+    return row_sched(bwd, S).G * row_U(bwd, S, edge);
+}
+// CTAs of T threads an SM holds at least (their register budget), and ring
+// stages.
+#ifndef GBN_FMINB
+#define GBN_FMINB 3
+#endif
+#ifndef GBN_FST
+#define GBN_FST 2
+#endif
+#ifndef GBN_BMINB
+#define GBN_BMINB 2
+#endif
+#ifndef GBN_BST
+#define GBN_BST 3
+#endif
 constexpr int fwd_minb(int S, bool edge)
 {
-    return kRow[S].T == 256 ? (kRow[S].KV == 1 && !edge ? 4 : 3)
-           : kRow[S].T == 512 && !edge ? 2 : 1;
+    const RowSched& e = kRowFwd[S];
+    return e.T == 256 ? (e.KV == 1 && !edge ? 4 : GBN_FMINB) : e.T == 512 && !edge ? 2 : 1;
 }
-constexpr int bwd_minb(int S) { return kRow[S].T == 256 ? 2 : 1; }
-constexpr int fwd_stages(int S) { return kRow[S].T == 256 ? 2 : 3; }
+constexpr int bwd_minb(int S) { return kRowBwd[S].T == 256 ? GBN_BMINB : 1; }
+constexpr int fwd_stages(int S) { return kRowFwd[S].T == 256 ? GBN_FST : 3; }
+constexpr int bwd_stages(int S) { return S == 9 ? 2 : GBN_BST; }
+// Registers a thread may use, from the CTAs asked for.
+constexpr int row_regs(int T, int minb) { return 65536 / (T * minb) / 8 * 8; }
 // Dynamic shared memory the kernels may ask for: three inputs of the widest
 // rows (32 KB each) in two stages, and room for the group maxima.
 constexpr int kMaxSmem = 208 * 1024;
-constexpr int bwd_stages(int S) { return kRow[S].T == 1024 ? 2 : 3; }
 
 #ifdef __CUDACC__
 
@@ -156,12 +205,13 @@ __device__ __forceinline__ void row_ring(const RowSrc (&in)[NT], const RowPlan& 
 }
 
 // --------------------------------------------------------------- vectors
-// Byte offset in the slot of row i (of the block from row r0 on): its first
-// vector, on a 16-byte boundary for the storage's vectors of 16 bytes.
+// Byte offset in the slot of the first element of row i of the block from row
+// r0 on.  CTAs step by a multiple of VEC rows, so for rows of activations it
+// is the same in every block of a CTA.
 __device__ __forceinline__ uint32_t row_off(const RowSrc& s, int64_t r0, int i)
 {
     const uint32_t rb = (uint32_t)s.row_bytes;
-    return (s.scattered ? 0u : (uint32_t)(r0 * s.row_bytes) & 15u) + (uint32_t)i * rb;
+    return (s.scattered ? 0u : ((uint32_t)r0 * rb) & 15u) + (uint32_t)i * rb;
 }
 
 __device__ __forceinline__ uint2 lds64(const void* p)
@@ -304,14 +354,15 @@ __device__ __forceinline__ void st_vec8(unsigned char* p, const uint32_t (&v)[VE
         __stcs(reinterpret_cast<unsigned*>(p), v[0]);
 }
 
-// A thread's part of its rows: element 0 of its vector j is column
-// col(j) = (l + j W) VEC - first, and em[j] says which of its elements are
-// the row's.
-template <int VEC, int W, int KV, bool kEdge>
+// A thread's part of its rows: its vector j is vector l + j W of the row,
+// whose element 0 is column col(j) = (l + j W) VEC - first, and em[j] says
+// which of its elements are the row's.
+template <int VEC, int KV, bool kEdge>
 struct Cols {
-    int l, first;
+    int l, W, first;
     uint32_t em[KV];
-    __device__ Cols(int lane, int first_, int N) : l(lane), first(kEdge ? first_ : 0)
+    __device__ Cols(int lane, int W_, int first_, int N)
+        : l(lane), W(W_), first(kEdge ? first_ : 0)
     {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
@@ -319,20 +370,50 @@ struct Cols {
             em[j] = hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
         }
     }
-    __device__ int col(int j) const { return (l + j * W) * VEC - first; }
+    __device__ int vec(int j) const { return l + j * W; }
+    __device__ int col(int j) const { return vec(j) * VEC - first; }
     __device__ bool ok(int j) const { return em[j] != 0; }
 };
 
 // Weights of a thread's vectors as float32 (1 + w for Gemma), zeros outside
-// the row.
-template <int VEC, int W, int KV, bool kEdge>
-__device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2], const Cols<VEC, W, KV, kEdge>& c,
+// the row.  Whole vectors of an aligned weight come as 16-byte loads.
+template <int VEC, int KV, bool kEdge>
+__device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2], const Cols<VEC, KV, kEdge>& c,
                                              const void* w, int wt, bool gemma)
 {
+    constexpr int P = VEC / 2;
+    const f2 one = splat2(gemma ? 1.f : 0.f);
+    if (!kEdge && (reinterpret_cast<uintptr_t>(w) & 15) == 0 && (VEC == 8 || wt == kF32)) {
+#pragma unroll
+        for (int j = 0; j < KV; ++j) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) wf[j][p] = splat2(0.f);
+            if (!c.ok(j)) continue;
+            if (wt == kF32) {
+#pragma unroll
+                for (int q = 0; q < P / 2; ++q) {
+                    const float4 v =
+                        __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c.col(j)) + q);
+                    wf[j][2 * q] = mk2(v.x, v.y);
+                    wf[j][2 * q + 1] = mk2(v.z, v.w);
+                }
+            } else if constexpr (VEC == 8) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                    static_cast<const unsigned short*>(w) + c.col(j)));
+                if (wt == kBF16)
+                    unpack2<__nv_bfloat16>(v, wf[j]);
+                else
+                    unpack2<__half>(v, wf[j]);
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) wf[j][p] = add2(wf[j][p], one);
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < KV; ++j)
 #pragma unroll
-        for (int p = 0; p < VEC / 2; ++p) {
+        for (int p = 0; p < P; ++p) {
             float v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -343,52 +424,90 @@ __device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2], const Cols<V
         }
 }
 
-// Sums (and NaN-keeping maxima) over the W threads of a row group, U rows at
-// once: every thread of a group gets the same bits.  Groups of several warps
-// join through `red` (2 x (T / W) x 2U x 32 floats, used in turn) with one
-// __syncthreads.
-template <int W, int T, int U, bool kMax>
-__device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* red, int& parity)
+// Sums (and NaN-keeping maxima) over a row group, U rows at once: every
+// thread of a group gets the same bits.  kW > 0: a group is kW <= 32 lanes of
+// a warp.  kW 0: a group of up to kWarps whole warps, joined through `red`
+// (row_red_floats, zero where no warp writes) with one __syncthreads; the two
+// halves of red are used in turn.
+template <int kW, int kWarps, int G, int U, bool kMax>
+__device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* red, int& parity,
+                                           int g, int l)
 {
-    constexpr int kIn = W < 32 ? W : 32;
+    constexpr int kIn = kW ? kW : 32;
     butterfly<kIn, U>(s);
-    if constexpr (kMax)
+    if constexpr (kMax) {
 #pragma unroll
         for (int off = kIn / 2; off >= 1; off >>= 1)
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 m[u] = max_nan(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
-    if constexpr (W > 32) {
-        constexpr int kWarps = W / 32, kG = T / W, kV = kMax ? 2 * U : U;
-        const int lane = threadIdx.x & 31, g = threadIdx.x / W, wig = (threadIdx.x % W) >> 5;
-        float* slot = red + (parity * kG + g) * kV * 32;
+    }
+    if constexpr (kW == 0) {
+        constexpr int kV = kMax ? 2 * U : U;
+        const int lane = threadIdx.x & 31;
+        float* slot = red + (parity * G + g) * kV * kWarps;
         if (lane == 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                slot[u * 32 + wig] = s[u];
-                if constexpr (kMax) slot[(U + u) * 32 + wig] = m[u];
+                slot[u * kWarps + (l >> 5)] = s[u];
+                if constexpr (kMax) slot[(U + u) * kWarps + (l >> 5)] = m[u];
             }
         }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            s[u] = slot[u * 32 + (lane & (kWarps - 1))];
-            if constexpr (kMax) m[u] = slot[(U + u) * 32 + (lane & (kWarps - 1))];
+            s[u] = slot[u * kWarps + (lane & (kWarps - 1))];
+            if constexpr (kMax) m[u] = slot[(U + u) * kWarps + (lane & (kWarps - 1))];
         }
         butterfly<kWarps, U>(s);
-        if constexpr (kMax)
+        if constexpr (kMax) {
 #pragma unroll
             for (int off = kWarps / 2; off >= 1; off >>= 1)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     m[u] = max_nan(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
+        }
         parity ^= 1;
     }
 }
-template <int W, int T, int U, bool kMax>
+template <int kW, int kWarps, int G, int U, bool kMax>
 constexpr int row_red_floats()
 {
-    return W > 32 ? 2 * (T / W) * (kMax ? 2 * U : U) * 32 : 1;
+    return kW ? 1 : 2 * G * (kMax ? 2 * U : U) * kWarps;
+}
+// Zero red; the caller's next __syncthreads publishes it.
+template <int kFloats>
+__device__ __forceinline__ void row_red_init(float* red)
+{
+    for (int i = threadIdx.x; i < kFloats; i += blockDim.x) red[i] = 0.f;
+}
+
+// Largest magnitude of a vector's elements, NaN on top, from its packed form:
+// 16-bit types compare in pairs (exact).
+template <typename TX>
+__device__ __forceinline__ float vec_amax(const uint4& v)
+{
+    if constexpr (is16<TX>()) {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t w[4] = {v.x & kAbs, v.y & kAbs, v.z & kAbs, v.w & kAbs};
+        uint32_t a, b, r;
+        if constexpr (std::is_same<TX, __half>::value) {
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        } else {
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        }
+        const f2 f = P16<TX>::to_f2(r);
+        return max_nan(lo2(f), hi2(f));
+    } else {
+        f2 p[2];
+        unpack2<TX>(v, p);
+        return max_nan(max_nan(fabsf(lo2(p[0])), fabsf(hi2(p[0]))),
+                       max_nan(fabsf(lo2(p[1])), fabsf(hi2(p[1]))));
+    }
 }
 
 // f(std::integral_constant<int, S>) for schedule sid.

@@ -65,10 +65,8 @@ __global__ void __launch_bounds__(kThreads)
             if (v + i * step >= whole) break;
             f2 o[P];
 #pragma unroll
-            for (int k = 0; k < VEC / 4; ++k) {
-                o[2 * k] = q8_unpack2(w[i][k] & 0xffffu, a.c.type);
-                o[2 * k + 1] = q8_unpack2(w[i][k] >> 16, a.c.type);
-            }
+            for (int k = 0; k < VEC / 4; ++k)
+                q8_unpack4(w[i][k], o[2 * k], o[2 * k + 1], a.c.type);
             const int end = cb[i] + VEC - 1;
             if (end < a.N && (end >> sh) == (cb[i] >> sh)) {
 #pragma unroll
@@ -87,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
     if (blockIdx.x == 0 && threadIdx.x < total - whole * VEC) {
         const int64_t i = whole * VEC + threadIdx.x, row = i / a.N;
         const float sc = a.c.scale[row * a.c.ng + ((int)(i - row * a.N) >> sh)];
-        st1(x, i, lo2(q8_unpack2(q[i], a.c.type)) * sc);
+        st1(x, i, q8_unpack1(q[i], a.c.type) * sc);
     }
 }
 

@@ -67,24 +67,17 @@ int64_t row_vectors(int64_t N, int vec, bool edge)
 {
     return edge ? (N + 2 * vec - 2) / vec : N / vec;
 }
-int find_sched(bool bwd, int64_t nvec)
+int find_sched(int64_t nvec)
 {
     for (int s = 0; s < gbn::kNumRowSched; ++s)
-        if (nvec <= gbn::row_sched(bwd, s).cap) return s;
+        if (nvec <= gbn::row_sched(false, s).cap) return s;
     return -1;
 }
 
-// CTAs of T threads on the device: as many as the kernel's register budget
-// (a launch bound) and, in the launch, shared memory allow.
-int64_t row_ctas(int sid, bool bwd, bool edge, int T, size_t smem, int sms)
+// CTAs the device holds at once.
+int64_t row_ctas(int sid, bool bwd, bool edge, int sms)
 {
-    const int minb = bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge);
-    int64_t per = 65536 / (gbn::row_regs(gbn::row_sched(bwd, sid).T, minb) * T);
-    if (smem) {
-        const int64_t fit = 227 * 1024 / (int64_t)(smem + 4096);  // its static part too
-        per = per < fit ? per : fit;
-    }
-    const int64_t ctas = (per < 1 ? 1 : per) * sms;
+    const int64_t ctas = (int64_t)sms * (bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge));
     // rows that start inside a vector need CTAs to step by a multiple of VEC rows
     return ctas >= 8 ? ctas / 8 * 8 : ctas;
 }
@@ -107,26 +100,29 @@ bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const Ro
             return false;
     }
     const int64_t nvec = row_vectors(N, vec, p.edge);
-    p.sid = find_sched(bwd, nvec);
+    p.sid = find_sched(nvec);
     if (p.sid < 0) return false;
     const gbn::RowSched& e = gbn::row_sched(bwd, p.sid);
-    p.W = gbn::row_W(bwd, p.sid, nvec);
-    p.R = gbn::row_R(bwd, p.sid, p.edge);
+    p.R = gbn::row_R(bwd, p.sid);
     p.stages = bwd ? gbn::bwd_stages(p.sid) : gbn::fwd_stages(p.sid);
     uint32_t at = 0;
+    p.plain = 1;
     for (int t = 0; t < nt; ++t) {
         p.off[t] = at;
-        if (in[t].p) at += (uint32_t)(p.R * in[t].row_bytes + 32 + 127) / 128 * 128;
+        if (!in[t].p) continue;
+        if (in[t].scattered || in[t].row_bytes % 16 != 0) p.plain = 0;
+        p.block_bytes += (uint32_t)(p.R * in[t].row_bytes);
+        at += (uint32_t)(p.R * in[t].row_bytes + 32 + 127) / 128 * 128;
     }
     p.stage_bytes = at;
     p.gm_off = 128 + p.stages * at;
     p.smem = p.gm_off + (p.edge && groups > 1 ? 2 * (size_t)p.R * groups * sizeof(float) : 0);
     if (bwd) {  // the CTA's column sums take the drained ring
-        const size_t cols = 128 + (size_t)p.W * e.G * e.KV * vec * sizeof(float);
+        const size_t cols = 128 + (size_t)e.T * e.KV * vec * sizeof(float);
         p.smem = p.smem > cols ? p.smem : cols;
     }
     p.nblocks = (M + p.R - 1) / p.R;
-    const int64_t cap = row_ctas(p.sid, bwd, p.edge, p.W * e.G, p.smem, sms);
+    const int64_t cap = row_ctas(p.sid, bwd, p.edge, sms);
     p.grid = (int)(p.nblocks < cap ? p.nblocks : cap);
     if (p.edge && p.nblocks > cap && cap * p.R % vec != 0) return false;
     return p.smem <= (size_t)gbn::kMaxSmem;
@@ -212,13 +208,13 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
         return GBN_EINVAL;
     const int sms = gbn::host_current_sms();
     if (sms <= 0) return GBN_EDEVICE;
+    if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
     gbn::RowPlan p{};
     const bool fast = M > 0 && plan_rows(p, true, xt, M, N, a.in, 3, {dx}, 0, sms);
     if (fast && !(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
     const int64_t P = M == 0 ? 0 : fast ? p.grid : gbn::add_bwd_general_rows(M, N, sms);
     if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
         return GBN_EWORKSPACE;
-    if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
     a.w = w;
     a.rstd = rstd;
     a.dx = dx;
@@ -251,12 +247,11 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
     const int vec = 16 / elem_bytes(xt);
     const bool edge = N % vec != 0;
     const int64_t nvec = row_vectors(N, vec, edge);
-    const int sid = find_sched(true, nvec);
+    const int sid = find_sched(nvec);
     int64_t P = add_bwd_general_rows(M, N, sms);
     if (sid >= 0) {
-        const int64_t R = row_R(true, sid, edge), blocks = (M + R - 1) / R;
-        const int T = row_W(true, sid, nvec) * row_sched(true, sid).G;
-        const int64_t cap = row_ctas(sid, true, edge, T, 0, sms);
+        const int64_t R = row_R(true, sid), blocks = (M + R - 1) / R;
+        const int64_t cap = row_ctas(sid, true, edge, sms);
         const int64_t grid = blocks < cap ? blocks : cap;
         P = P > grid ? P : grid;
     }

@@ -9,29 +9,26 @@ namespace gbn {
 namespace {
 
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
+__global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
     add_bwd_ring(const __grid_constant__ BwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int kW = kRowBwd[S].W, G = kRowBwd[S].G, KV = kRowBwd[S].KV;
-    constexpr int U = row_U(true, S, kEdge), R = G * U, kWarps = kRowBwd[S].T / G / 32;
+    constexpr int W = kRowB[S].W, T = kRowB[S].T, KV = kRowB[S].KV, G = row_G(true, S);
+    constexpr int U = row_U(true, S), R = row_R(true, S);
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
-    constexpr bool kPacked = kMode == kBwdC, kCast = kMode == kBwdCast, kLean = row_lean(S);
+    constexpr bool kPacked = kMode == kBwdC, kCast = kMode == kBwdCast, kLean = KV > 2;
     // words of a thread's vector of s: activations, or 8-bit codes
     constexpr int NS = kPacked ? VEC / 4 : 4, VS = kPacked ? VEC : 16, ES = kPacked ? 1 : E;
-    constexpr int kRed = row_red_floats<kW, kWarps, G, U, false>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[kRed];
+    __shared__ float red[row_red_floats<W, T, U, false>()];
     int parity = 0;
-    const int N = a.N, W = kW ? kW : pl.W;
-    const int g = G == 1 ? 0 : threadIdx.x / W, l = threadIdx.x - g * W;
-    if constexpr (kW == 0) row_red_init<kRed>(red);
+    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
 
     int64_t row = (int64_t)blockIdx.x * R + g;  // this thread's first row
-    const Cols<VEC, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
+    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P], acc[KV][P];
-    load_weights<VEC, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
 #pragma unroll
     for (int j = 0; j < KV; ++j)
 #pragma unroll
@@ -47,33 +44,27 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
 
     // A row's rstd, and the scales of its vectors' groups, are loaded one row
     // block ahead of their use.  kEdge: elements from eb on take the second.
-    int ga[KV], eb[KV];
-    if constexpr (kPacked) {
-#pragma unroll
-        for (int j = 0; j < KV; ++j) {
-            const int c = cols.col(j) < 0 ? 0 : cols.col(j);
-            const bool whole = a.c.shift == 31;
-            ga[j] = whole ? 0 : c >> a.c.shift;
-            eb[j] = kEdge && !whole ? ((ga[j] + 1) << a.c.shift) - cols.col(j) : VEC;
-        }
-    }
+    const bool whole = !kPacked || a.c.shift == 31;
+    auto group_of = [&](int j) {
+        const int c = cols.col(j) < 0 ? 0 : cols.col(j);
+        return whole ? 0 : c >> a.c.shift;
+    };
     constexpr int kSc = kPacked ? (kEdge ? 2 : 1) : 0;
     float rs_n[U], sc_n[U][KV][kSc ? kSc : 1];
     auto load_stats = [&](int64_t row0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = row0 + u * G;
-            const bool ok = r < a.M;
-            rs_n[u] = ok ? __ldca(a.rstd + r) : 0.f;
+            const bool in = r < a.M;
+            rs_n[u] = in ? __ldca(a.rstd + r) : 0.f;
             if constexpr (kPacked) {
                 const float* const scr = a.c.scale + r * a.c.ng;
 #pragma unroll
                 for (int j = 0; j < KV; ++j) {
-                    const bool in = ok && cols.ok(j);
-                    sc_n[u][j][0] = in ? __ldca(scr + ga[j]) : 0.f;
+                    const int q = group_of(j);
+                    sc_n[u][j][0] = in && cols.ok(j) ? __ldca(scr + q) : 0.f;
                     if constexpr (kEdge)
-                        sc_n[u][j][1] =
-                            in && eb[j] < VEC && ga[j] + 1 < a.c.ng ? __ldca(scr + ga[j] + 1) : 0.f;
+                        sc_n[u][j][1] = in && cols.ok(j) && q + 1 < a.c.ng ? __ldca(scr + q + 1) : 0.f;
                 }
             }
         }
@@ -94,26 +85,22 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
 #pragma unroll
                 for (int j = 0; j < KV; ++j)
 #pragma unroll
-                    for (int q = 0; q < kSc; ++q) sc[u][j][q] = sc_n[u][j][q];
+                    for (int q = 0; q < kSc; ++q) sc[u][j][q] = sc_n[u][j][q] * rs[u];
             }
         }
         auto ld_s = [&](int u, int j, uint32_t (&v)[NS]) {
             const bool ok = okr[u] && cols.ok(j);
-            const int64_t e = at + (int64_t)u * G * N + j * W * VEC;
             const uint32_t o = so0 + u * G * (uint32_t)a.in[0].row_bytes + j * W * VS;
             if constexpr (kPacked) {
-                ld_vec8<VEC, kEdge>(v, slot, sc0 + o, ok, a.in[0], last, e, cols.em[j]);
+                ld_vec8<VEC, kEdge>(v, slot, sc0 + o, ok, cols.em[j]);
             } else {
-                const uint4 q =
-                    ld_vec<TX, kEdge>(slot, o, ok, a.in[0], last, e * E, cols.em[j]);
+                const uint4 q = ld_vec<TX, kEdge>(slot, o, ok, cols.em[j]);
                 v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
             }
         };
-        auto ld_act = [&](int u, int j, int t, uint32_t so) {
-            const bool ok = okr[u] && cols.ok(j) && (t == 1 || a.in[2].p);
-            const int64_t e = at + (int64_t)u * G * N + j * W * VEC;
+        auto ld_act = [&](int u, int j, bool present, uint32_t so) {
             const uint32_t o = so + u * G * (uint32_t)a.in[1].row_bytes + j * W * 16;
-            return ld_vec<TX, kEdge>(slot, o, ok, a.in[t], last, e * E, cols.em[j]);
+            return ld_vec<TX, kEdge>(slot, o, okr[u] && cols.ok(j) && present, cols.em[j]);
         };
         uint32_t sp[U][KV][NS];
         uint4 dyp[U][KV], dsp[U][KV];
@@ -123,8 +110,8 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
 #pragma unroll
                 for (int j = 0; j < KV; ++j) {
                     ld_s(u, j, sp[u][j]);
-                    dyp[u][j] = ld_act(u, j, 1, so1);
-                    dsp[u][j] = ld_act(u, j, 2, so2);
+                    dyp[u][j] = ld_act(u, j, true, so1);
+                    dsp[u][j] = ld_act(u, j, a.in[2].p != nullptr, so2);
                 }
         }
         load_stats(row + row_step);
@@ -132,22 +119,21 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
         auto terms = [&](int u, int j, f2 (&xh)[P], f2 (&dn)[P], f2 (&dv)[P]) {
             if constexpr (kLean) {
                 ld_s(u, j, sp[u][j]);
-                dyp[u][j] = ld_act(u, j, 1, so1);
+                dyp[u][j] = ld_act(u, j, true, so1);
             }
             if constexpr (kPacked) {
 #pragma unroll
                 for (int i = 0; i < VEC / 4; ++i)
                     q8_unpack4(sp[u][j][i], xh[2 * i], xh[2 * i + 1], a.c.type);
-                const float ka = sc[u][j][0] * rs[u];
                 if constexpr (kEdge) {
-                    const float kb = sc[u][j][kSc - 1] * rs[u];
+                    const int eb = whole ? VEC : ((group_of(j) + 1) << a.c.shift) - cols.col(j);
+                    const float ka = sc[u][j][0], kb = sc[u][j][kSc - 1];
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        xh[p] = mul2(xh[p], mk2(2 * p < eb[j] ? ka : kb,
-                                                2 * p + 1 < eb[j] ? ka : kb));
+                        xh[p] = mul2(xh[p], mk2(2 * p < eb ? ka : kb, 2 * p + 1 < eb ? ka : kb));
                 } else {
 #pragma unroll
-                    for (int p = 0; p < P; ++p) xh[p] = mul2(xh[p], splat2(ka));
+                    for (int p = 0; p < P; ++p) xh[p] = mul2(xh[p], splat2(sc[u][j][0]));
                 }
             } else {
                 unpack2<TX>(make_uint4(sp[u][j][0], sp[u][j][1], sp[u][j][2], sp[u][j][3]), xh);
@@ -166,6 +152,7 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
             f2 q = splat2(0.f);
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
+                if (KV > 1 && j >= cols.live) continue;
                 f2 xh[P], dn[P], dv[P];
                 terms(u, j, xh, dn, dv);
 #pragma unroll
@@ -184,16 +171,17 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
             }
             sum[u] = lo2(q) + hi2(q);
         }
-        row_reduce<kW, kWarps, G, U, false>(sum, none, red, parity, g, l);
+        row_reduce<W, T, U, false>(sum, none, red, parity, g, l);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const f2 r2 = splat2(rs[u]), nm = splat2(-(sum[u] * a.inv_n));
             TX* const dxr = static_cast<TX*>(a.dx) + at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
+                if (KV > 1 && j >= cols.live) continue;
                 f2 xh[P], dn[P], dv[P];
                 terms(u, j, xh, dn, dv);
-                if constexpr (kLean) dsp[u][j] = ld_act(u, j, 2, so2);
+                if constexpr (kLean) dsp[u][j] = ld_act(u, j, a.in[2].p != nullptr, so2);
                 unpack2<TX>(dsp[u][j], dv);
 #pragma unroll
                 for (int p = 0; p < P; ++p) dv[p] = fma2(r2, fma2(xh[p], nm, dn[p]), dv[p]);
@@ -203,14 +191,14 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
         }
         row += row_step;
         at += at_step;
-        return kW == 0 && !kLean;  // row_reduce's barrier came after the last slot read
+        return W > 32 && !kLean;  // row_reduce's barrier came after the last slot read
     });
 
     if (a.ws == nullptr) return;  // no weight gradient wanted (uniform)
     // The CTA's column sums, its row groups added in order: each group leaves
     // its vectors in the drained ring, and column c of group q is found
     // `first` of that group's rows further on.
-    const int cap = W * KV * VEC;
+    constexpr int cap = W * KV * VEC;
     float* const out = a.ws + blockIdx.x * (int64_t)N;
     if constexpr (G == 1) {
 #pragma unroll
@@ -230,7 +218,7 @@ __global__ void __launch_bounds__(kRowBwd[S].T, bwd_minb(S))
                 *reinterpret_cast<float2*>(buf + g * cap + cols.vec(j) * VEC + 2 * p) =
                     make_float2(lo2(acc[j][p]), hi2(acc[j][p]));
         __syncthreads();
-        for (int c = threadIdx.x; c < N; c += blockDim.x) {
+        for (int c = threadIdx.x; c < N; c += T) {
             float t = 0.f;
 #pragma unroll 4
             for (int q = 0; q < G; ++q) {
@@ -249,7 +237,7 @@ cudaError_t bwd_launch(cudaStream_t st, int mode, const BwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_bwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * kRowBwd[S].G, p.smem, st, a, p);
+        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, kRowB[S].T, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -28,28 +28,25 @@ __device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v
 }
 
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
+__global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
     add_fwd_ring(const __grid_constant__ FwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int kW = kRowFwd[S].W, G = kRowFwd[S].G, KV = kRowFwd[S].KV;
-    constexpr int U = row_U(false, S, kEdge), R = G * U, kWarps = kRowFwd[S].T / G / 32;
+    constexpr int W = kRowF[S].W, T = kRowF[S].T, KV = kRowF[S].KV, G = row_G(false, S);
+    constexpr int U = row_U(false, S), R = row_R(false, S);
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
     constexpr bool kNorm = kMode != kModeC, kMax = kMode != kModeY;
-    constexpr int kRed = row_red_floats<kW, kWarps, G, U, kMax>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[kRed];
+    __shared__ float red[row_red_floats<W, T, U, kMax>()];
     int parity = 0;
-    const int N = a.N, W = kW ? kW : pl.W;
-    const int g = G == 1 ? 0 : threadIdx.x / W, l = threadIdx.x - g * W;
-    if constexpr (kW == 0) row_red_init<kRed>(red);
+    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
 
     // the first row of this thread; its later ones are a multiple of VEC rows on
     int64_t row = (int64_t)blockIdx.x * R + g;
-    const Cols<VEC, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
+    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P];
-    if constexpr (kNorm) load_weights<VEC, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    if constexpr (kNorm) load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
     // this thread's first vector: its element in the [M, N] tensors, and its
     // byte in a slot (rows of a slot are row_bytes apart)
     int64_t at = row * N - cols.first + l * VEC;
@@ -76,7 +73,7 @@ __global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
             lead[j] = cols.ok(j) && (c & (whole ? -1 : (1 << q8.shift) - 1)) == 0;
         }
         if (shared_max) {
-            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += blockDim.x) gm[i] = 0.f;
+            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += T) gm[i] = 0.f;
             __syncthreads();
         }
     }
@@ -95,13 +92,14 @@ __global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
             TX* const sr = static_cast<TX*>(a.s) + at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
+                gmx[u][j] = 0.f;
+                sp[u][j] = make_uint4(0, 0, 0, 0);
+                if (KV > 1 && j >= cols.live) continue;
                 const bool ok = okr[u] && cols.ok(j);
                 const uint32_t o = u * srow + j * W * 16;
-                const int64_t gb = (at + (int64_t)u * G * N + j * W * VEC) * E;
-                sp[u][j] = ld_vec<TX, kEdge>(slot, so0 + o, ok, a.in[0], last, gb, cols.em[j]);
+                sp[u][j] = ld_vec<TX, kEdge>(slot, so0 + o, ok, cols.em[j]);
                 if (a.in[1].p) {
-                    const uint4 rv =
-                        ld_vec<TX, kEdge>(slot, so1 + o, ok, a.in[1], last, gb, cols.em[j]);
+                    const uint4 rv = ld_vec<TX, kEdge>(slot, so1 + o, ok, cols.em[j]);
                     f2 xa[P], xb[P];
                     unpack2<TX>(sp[u][j], xa);
                     unpack2<TX>(rv, xb);
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
         }
         // the row's sum, and its maximum for a scale per row; a group's
         // maximum from its lanes, or from shared memory
-        if (kNorm || whole) row_reduce<kW, kWarps, G, U, kMax>(ss, mx, red, parity, g, l);
+        if (kNorm || whole) row_reduce<W, T, U, kMax>(ss, mx, red, parity, g, l);
         if constexpr (kMax) {
             if (shared_max) {
                 __syncthreads();
@@ -176,6 +174,7 @@ __global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
             const int64_t atu = at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
+                if (KV > 1 && j >= cols.live) continue;
                 const bool ok = okr[u] && cols.ok(j);
                 f2 sv[P];
                 unpack2<TX>(sp[u][j], sv);
@@ -227,10 +226,10 @@ __global__ void __launch_bounds__(kRowFwd[S].T, fwd_minb(S, kEdge))
         if (shared_max) {
             // the other half is free: its readers passed the barrier above
             half ^= 1;
-            for (int i = threadIdx.x; i < R * q8.ng; i += blockDim.x) gm[half * R * q8.ng + i] = 0.f;
+            for (int i = threadIdx.x; i < R * q8.ng; i += T) gm[half * R * q8.ng + i] = 0.f;
             return false;  // and a barrier before its next use
         }
-        return kW == 0 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
+        return W > 32 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
     });
 }
 
@@ -241,7 +240,7 @@ cudaError_t fwd_launch(cudaStream_t st, int mode, const FwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_fwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * kRowFwd[S].G, p.smem, st, a, p);
+        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, kRowF[S].T, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -73,7 +73,9 @@ struct UnpackArgs {
 // blocks of R rows through a ring of `stages` stages, each holding one block
 // of every input at off[t].
 struct RowPlan {
-    int sid, edge, grid, W;
+    int sid, edge, grid;
+    int plain;             // every input's rows in order, of whole 16-byte units
+    uint32_t block_bytes;  // of a whole block, all inputs
     int64_t nblocks;
     int R, stages;
     uint32_t off[3], stage_bytes, gm_off;  // gm_off: the group maxima's place

@@ -8,7 +8,7 @@
 // rows of any length: a block that does not start or end on a 16-byte
 // boundary is copied from the boundary below to the one above it, clipped to
 // the input's whole 16-byte units; what lies past those (the input's last 15
-// bytes at most) is read from global memory by the last block.
+// bytes at most) the last block's threads put into the slot themselves.
 //
 // Vectors.  A row of N elements starts at element r N of a contiguous tensor.
 // The vectors are those of the storage: VEC elements from a multiple of VEC
@@ -23,78 +23,57 @@
 
 namespace gbn {
 
-// Schedules.  A row of nvec vectors goes to a row group of W threads with KV
-// vectors each (vector v of the row to thread v % W); a CTA has G groups.  Up
-// to 64 vectors a group is (part of) a warp, with W the next power of two;
-// wider rows take as many warps as they fill, W = 32 ceil(nvec / (32 KV)), so
-// that no more than a warp's worth of lanes idles.  Two vectors a thread
-// halve the reduction that one would take.  The widest backward holds its
-// column sums and weights in registers (T <= 512 leaves 128 each) and reads
-// its row from the ring once more instead of keeping it (row_lean).
+// Schedules.  A row of up to `cap` vectors goes to a row group of W threads
+// with KV vectors each (vector v of the row to thread v % W); a CTA of T
+// threads has G = T / W groups.  Up to 32 vectors: one a lane.  From there on
+// several a thread, so that the row reduction, its barrier and the ring's work
+// per row are shared by them: four in the forwards (rows of up to 128 vectors
+// stay in one warp), two in the backwards, which hold a column sum and a
+// weight of every element next to the row.  The widest backward holds four
+// column sums and weights and reads its row from the ring a second time
+// instead of keeping it.  A warp skips those of its KV vectors that lie past
+// the row's end.
 struct RowSched {
-    int cap, W, G, KV, T;  // W 0: as many warps as the row fills, T / G threads at most
+    int cap, W, KV, T;
 };
 constexpr int kNumRowSched = 10;
-constexpr RowSched kRowFwd[kNumRowSched] = {
-    {4, 4, 64, 1, 256},    {8, 8, 32, 1, 256},   {16, 16, 16, 1, 256}, {32, 32, 8, 1, 256},
-    {64, 32, 8, 2, 256},   {128, 0, 4, 2, 256},  {256, 0, 2, 2, 256},  {512, 0, 1, 2, 256},
-    {1024, 0, 1, 2, 512},  {2048, 0, 1, 2, 1024},
+constexpr RowSched kRowF[kNumRowSched] = {
+    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
+    {64, 32, 2, 256},  {128, 32, 4, 256}, {256, 64, 4, 256},  {512, 128, 4, 256},
+    {1024, 256, 4, 256}, {2048, 512, 4, 512},
 };
-constexpr RowSched kRowBwd[kNumRowSched] = {
-    {4, 4, 64, 1, 256},    {8, 8, 32, 1, 256},   {16, 16, 16, 1, 256}, {32, 32, 8, 1, 256},
-    {64, 32, 8, 2, 256},   {128, 0, 4, 2, 256},  {256, 0, 2, 2, 256},  {512, 0, 1, 2, 256},
-    {1024, 0, 1, 2, 512},  {2048, 0, 1, 4, 512},
+constexpr RowSched kRowB[kNumRowSched] = {
+    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
+    {64, 32, 2, 256},  {128, 64, 2, 256}, {256, 128, 2, 256}, {512, 256, 2, 256},
+    {1024, 512, 2, 512}, {2048, 512, 4, 512},
 };
-constexpr const RowSched& row_sched(bool bwd, int S) { return bwd ? kRowBwd[S] : kRowFwd[S]; }
-constexpr int row_W(bool bwd, int S, int64_t nvec)
-{
-    const RowSched& e = row_sched(bwd, S);
-    return e.W ? e.W : (int)((nvec + 32 * e.KV - 1) / (32 * e.KV)) * 32;
-}
-constexpr bool row_lean(int S) { return S == 9; }
-#ifndef GBN_FU
-#define GBN_FU 1
+constexpr const RowSched& row_sched(bool bwd, int S) { return bwd ? kRowB[S] : kRowF[S]; }
+constexpr int row_G(bool bwd, int S) { return row_sched(bwd, S).T / row_sched(bwd, S).W; }
+// Rows a thread takes of a block: two of one vector.  (A thread's rows of a
+// block are G apart, a multiple of VEC: rows that start inside a vector keep
+// one mask and one set of weights a thread.)
+constexpr int row_U(bool bwd, int S) { return row_sched(bwd, S).KV == 1 ? 2 : 1; }
+constexpr int row_R(bool bwd, int S) { return row_G(bwd, S) * row_U(bwd, S); }
+// CTAs an SM holds at least (their register budget), and ring stages.
+#ifndef GBN_FMINB1
+#define GBN_FMINB1 4
 #endif
-#ifndef GBN_BU
-#define GBN_BU 1
-#endif
-// Rows a thread takes of a block.  Rows that start inside a vector keep one
-// mask and one set of weights a thread, so a thread's rows of a block are a
-// multiple of VEC rows apart (G) or one.
-constexpr int row_U(bool bwd, int S, bool edge)
-{
-    const RowSched& e = row_sched(bwd, S);
-    return e.KV == 1 ? 2 : e.T > 512 || e.KV > 2 || (edge && e.G % 8 != 0) ? 1
-           : bwd ? GBN_BU : GBN_FU;
-}
-constexpr int row_R(bool bwd, int S, bool edge)
-{
-    return row_sched(bwd, S).G * row_U(bwd, S, edge);
-}
-// CTAs of T threads an SM holds at least (their register budget), and ring
-// stages.
-#ifndef GBN_FMINB
-#define GBN_FMINB 3
+#ifndef GBN_FST1
+#define GBN_FST1 2
 #endif
 #ifndef GBN_FST
 #define GBN_FST 2
-#endif
-#ifndef GBN_BMINB
-#define GBN_BMINB 2
 #endif
 #ifndef GBN_BST
 #define GBN_BST 3
 #endif
 constexpr int fwd_minb(int S, bool edge)
 {
-    const RowSched& e = kRowFwd[S];
-    return e.T == 256 ? (e.KV == 1 && !edge ? 4 : GBN_FMINB) : e.T == 512 && !edge ? 2 : 1;
+    return kRowF[S].T == 512 ? 1 : kRowF[S].KV > 1 ? 2 : edge ? 3 : GBN_FMINB1;
 }
-constexpr int bwd_minb(int S) { return kRowBwd[S].T == 256 ? GBN_BMINB : 1; }
-constexpr int fwd_stages(int S) { return kRowFwd[S].T == 256 ? GBN_FST : 3; }
-constexpr int bwd_stages(int S) { return S == 9 ? 2 : GBN_BST; }
-// Registers a thread may use, from the CTAs asked for.
-constexpr int row_regs(int T, int minb) { return 65536 / (T * minb) / 8 * 8; }
+constexpr int bwd_minb(int S) { return kRowB[S].T == 512 ? 1 : 2; }
+constexpr int fwd_stages(int S) { return kRowF[S].KV == 1 ? GBN_FST1 : GBN_FST; }
+constexpr int bwd_stages(int S) { return kRowB[S].KV == 4 ? 2 : GBN_BST; }
 // Dynamic shared memory the kernels may ask for: three inputs of the widest
 // rows (32 KB each) in two stages, and room for the group maxima.
 constexpr int kMaxSmem = 208 * 1024;
@@ -102,6 +81,21 @@ constexpr int kMaxSmem = 208 * 1024;
 #ifdef __CUDACC__
 
 // ------------------------------------------------------------------ ring
+// Byte range of block b of a contiguous input that a bulk copy moves, and the
+// end of its rows.
+struct Span {
+    int64_t start, end, rows_end;
+};
+__device__ __forceinline__ Span row_span(const RowSrc& s, int64_t r0, int rows)
+{
+    Span p;
+    p.start = (r0 * s.row_bytes) & ~(int64_t)15;
+    p.rows_end = (r0 + rows) * s.row_bytes;
+    const int64_t whole = s.total & ~(int64_t)15, up = (p.rows_end + 15) & ~(int64_t)15;
+    p.end = up < whole ? up : whole;
+    return p;
+}
+
 // Block b into stage st: every lane of warp 0.
 template <int NT>
 __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan& pl, int64_t M,
@@ -111,6 +105,20 @@ __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan&
     unsigned char* const slot = dsm + 128 + (size_t)st * pl.stage_bytes;
     const int lane = threadIdx.x & 31;
     const int64_t r0 = b * pl.R;
+    if (pl.plain && b < pl.nblocks - 1) {
+        // a whole block of rows in order, each of whole 16-byte units: the
+        // usual case, one lane with a product and a copy per input
+        if (lane == 0) {
+            mbar_expect_tx(bar, pl.block_bytes);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (in[t].p) {
+                    const uint32_t n = (uint32_t)pl.R * (uint32_t)in[t].row_bytes;
+                    bulk_g2s(slot + pl.off[t], in[t].p + b * (int64_t)n, n, bar);
+                }
+        }
+        return;
+    }
     const int rows = (int)(M - r0 < pl.R ? M - r0 : pl.R);
     int64_t start[NT];
     uint32_t n[NT], sum = 0;
@@ -123,11 +131,9 @@ __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan&
             scattered = true;
             n[t] = (uint32_t)(rows * in[t].row_bytes);
         } else {
-            start[t] = (r0 * in[t].row_bytes) & ~(int64_t)15;
-            int64_t end = ((r0 + rows) * in[t].row_bytes + 15) & ~(int64_t)15;
-            const int64_t whole = in[t].total & ~(int64_t)15;
-            end = end < whole ? end : whole;
-            n[t] = end > start[t] ? (uint32_t)(end - start[t]) : 0;
+            const Span sp = row_span(in[t], r0, rows);
+            start[t] = sp.start;
+            n[t] = sp.end > sp.start ? (uint32_t)(sp.end - sp.start) : 0;
         }
         sum += n[t];
     }
@@ -146,6 +152,25 @@ __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan&
                     bulk_g2s(slot + pl.off[t] + i * (uint32_t)in[t].row_bytes,
                              in[t].p + row_byte_offset(in[t].map, r0 + i),
                              (uint32_t)in[t].row_bytes, bar);
+    }
+}
+
+// The bytes of block b past the inputs' whole 16-byte units, into the slot:
+// every thread, once the block's copies have landed; the caller synchronizes.
+template <int NT>
+__device__ __noinline__ void row_tail(const RowSrc (&in)[NT], const RowPlan& pl, int64_t M,
+                                      unsigned char* slot, int64_t b)
+{
+    const int64_t r0 = b * pl.R;
+    const int rows = (int)(M - r0 < pl.R ? M - r0 : pl.R);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        if (!in[t].p || in[t].scattered) continue;
+        const Span sp = row_span(in[t], r0, rows);
+        const int64_t from = sp.end > sp.start ? sp.end : sp.start;
+        if (from >= sp.rows_end) continue;
+        const int i = threadIdx.x;
+        if (from + i < sp.rows_end) slot[pl.off[t] + (from - sp.start) + i] = in[t].p[from + i];
     }
 }
 
@@ -183,11 +208,16 @@ __device__ __forceinline__ void row_ring(const RowSrc (&in)[NT], const RowPlan& 
     bool alive = true;
     int64_t failed_at = K, b = blockIdx.x;
     for (int64_t k = 0; k < K; ++k) {
+        unsigned char* const slot = dsm + 128 + (size_t)st * pl.stage_bytes;
         if (alive) {
             alive = mbar_wait(&bar[st], phase, pl.fault);
             if (!alive) failed_at = k;
         }
-        if (!body(b, dsm + 128 + (size_t)st * pl.stage_bytes, alive)) __syncthreads();
+        if (!pl.plain && b == pl.nblocks - 1) {  // uniform; a failed wait loads nothing below
+            row_tail(in, pl, M, slot, b);
+            __syncthreads();
+        }
+        if (!body(b, slot, alive)) __syncthreads();
         if (threadIdx.x < 32 && alive && k + pl.stages < K) {
             fence_proxy_async();
             row_issue(in, pl, M, dsm, b + (int64_t)pl.stages * gridDim.x, st);
@@ -227,89 +257,55 @@ __device__ __forceinline__ uint32_t lds32(const void* p)
     return v;
 }
 
-// The bytes of vector `gb` (its byte offset in a contiguous input) that the
-// ring did not copy, one element of E bytes at a time; elements outside the
-// mask are zeros.
-template <int E, int VEC, int NW>
-__device__ __forceinline__ void gather_tail(const RowSrc& s, int64_t gb, uint32_t em,
-                                            uint32_t (&v)[NW])
-{
-#pragma unroll
-    for (int i = 0; i < NW; ++i) v[i] = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-        if ((em >> e) & 1u) {
-            const unsigned char* p = s.p + gb + e * E;
-            if constexpr (E == 1)
-                v[e / 4] |= (uint32_t)*p << (8 * (e % 4));
-            else if constexpr (E == 2)
-                v[e / 2] |= (uint32_t)*reinterpret_cast<const unsigned short*>(p) << (16 * (e % 2));
-            else
-                v[e] = *reinterpret_cast<const uint32_t*>(p);
-        }
-}
-
-// Words of the elements in the mask, zeros for the others.
+// A vector's words of NW words with the elements outside the mask zeroed;
+// Mask holds one word of bits per word.
 template <int VEC, int NW>
-__device__ __forceinline__ void mask_words(uint32_t (&v)[NW], uint32_t em)
-{
-    constexpr int per = VEC / NW;  // elements a word
+struct Mask {
+    uint32_t m[NW];
+    __device__ explicit Mask(uint32_t em)
+    {
+        constexpr int per = VEC / NW, bits = 32 / per;  // elements a word
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        uint32_t m = 0;
+        for (int i = 0; i < NW; ++i) {
+            m[i] = 0;
 #pragma unroll
-        for (int e = 0; e < per; ++e)
-            if ((em >> (i * per + e)) & 1u) m |= (per == 1 ? ~0u : ((1u << (32 / per)) - 1u)) << (e * (32 / per) % 32);
-        v[i] &= m;
-    }
-}
-
-// Vector at byte `off` of the slot (16 bytes of activations).  `last`: the
-// block may reach past the copied bytes; gb is then its byte offset in the
-// input.
-template <typename TX, bool kEdge>
-__device__ __forceinline__ uint4 ld_vec(const unsigned char* slot, uint32_t off, bool ok,
-                                        const RowSrc& s, bool last, int64_t gb, uint32_t em)
-{
-    if constexpr (kEdge) {
-        uint32_t v[4] = {0, 0, 0, 0};
-        if (ok) {
-            if (last && gb + 16 > (s.total & ~(int64_t)15)) {
-                gather_tail<sizeof(TX), Vec<TX>::kN>(s, gb, em, v);
-            } else {
-                const uint4 q = lds128(slot + off);
-                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-                if (em != (1u << Vec<TX>::kN) - 1u) mask_words<Vec<TX>::kN>(v, em);
-            }
+            for (int e = 0; e < per; ++e)
+                if ((em >> (i * per + e)) & 1u)
+                    m[i] |= (per == 1 ? ~0u : (1u << (bits % 32)) - 1u) << (e * bits % 32);
         }
-        return make_uint4(v[0], v[1], v[2], v[3]);
-    } else {
-        return lds128_if(ok, slot + off);
     }
+};
+
+// 16 bytes of activations at byte o of the slot; kEdge: masked.
+template <typename TX, bool kEdge>
+__device__ __forceinline__ uint4 ld_vec(const unsigned char* slot, uint32_t o, bool ok,
+                                        uint32_t em)
+{
+    uint4 v = lds128_if(ok, slot + o);
+    if constexpr (kEdge) {
+        const Mask<Vec<TX>::kN, 4> k(em);
+        v.x &= k.m[0], v.y &= k.m[1], v.z &= k.m[2], v.w &= k.m[3];
+    }
+    return v;
 }
 
-// A vector's VEC 8-bit values, from the slot (or past the copied bytes).
+// A vector's VEC 8-bit values.
 template <int VEC, bool kEdge>
 __device__ __forceinline__ void ld_vec8(uint32_t (&v)[VEC / 4], const unsigned char* slot,
-                                        uint32_t off, bool ok, const RowSrc& s, bool last,
-                                        int64_t gb, uint32_t em)
+                                        uint32_t o, bool ok, uint32_t em)
 {
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) v[i] = 0;
-    if (!ok) return;
-    if (last && gb + VEC > (s.total & ~(int64_t)15)) {
-        gather_tail<1, VEC>(s, gb, em, v);
-        return;
-    }
     if constexpr (VEC == 8) {
-        const uint2 q = lds64(slot + off);
+        const uint2 q = ok ? lds64(slot + o) : make_uint2(0, 0);
         v[0] = q.x;
         v[1] = q.y;
     } else {
-        v[0] = lds32(slot + off);
+        v[0] = ok ? lds32(slot + o) : 0u;
     }
-    if constexpr (kEdge)
-        if (em != (1u << VEC) - 1u) mask_words<VEC>(v, em);
+    if constexpr (kEdge) {
+        const Mask<VEC, VEC / 4> k(em);
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) v[i] &= k.m[i];
+    }
 }
 
 // Store a vector of activations: whole, or the elements in the mask.
@@ -322,16 +318,18 @@ __device__ __forceinline__ void st_vec(TX* p, const uint4& v, bool ok, uint32_t 
             st_stream(p, v);
             return;
         }
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < Vec<TX>::kN; ++e)
-            if ((em >> e) & 1u) {
-                if constexpr (sizeof(TX) == 2)
-                    reinterpret_cast<unsigned short*>(p)[e] =
-                        (unsigned short)(w[e / 2] >> (16 * (e % 2)));
-                else
-                    reinterpret_cast<uint32_t*>(p)[e] = w[e];
-            }
+        // by halves, an element a turn: little code for the one lane in many
+        uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+        constexpr int kHalf = Vec<TX>::kN / 2, kBits = 64 / kHalf;
+        using W = typename std::conditional<sizeof(TX) == 2, unsigned short, uint32_t>::type;
+        W* const q = reinterpret_cast<W*>(p);
+#pragma unroll 1
+        for (int e = 0; e < kHalf; ++e) {
+            if ((em >> e) & 1u) q[e] = (W)lo;
+            if ((em >> (kHalf + e)) & 1u) q[kHalf + e] = (W)hi;
+            lo >>= kBits;
+            hi >>= kBits;
+        }
     } else {
         st_stream_if(ok, p, v);
     }
@@ -343,9 +341,12 @@ __device__ __forceinline__ void st_vec8(unsigned char* p, const uint32_t (&v)[VE
 {
     if (!ok) return;
     if (kEdge && em != (1u << VEC) - 1u) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if ((em >> e) & 1u) p[e] = (unsigned char)(v[e / 4] >> (8 * (e % 4)));
+        uint64_t w = VEC == 8 ? (uint64_t)v[VEC / 4 - 1] << 32 | v[0] : v[0];
+#pragma unroll 1
+        for (int e = 0; e < VEC; ++e) {
+            if ((em >> e) & 1u) p[e] = (unsigned char)w;
+            w >>= 8;
+        }
         return;
     }
     if constexpr (VEC == 8)
@@ -356,18 +357,19 @@ __device__ __forceinline__ void st_vec8(unsigned char* p, const uint32_t (&v)[VE
 
 // A thread's part of its rows: its vector j is vector l + j W of the row,
 // whose element 0 is column col(j) = (l + j W) VEC - first, and em[j] says
-// which of its elements are the row's.
-template <int VEC, int KV, bool kEdge>
+// which of its elements are the row's.  The first `live` of them have a lane
+// of this warp in the row.
+template <int VEC, int W, int KV, bool kEdge>
 struct Cols {
-    int l, W, first;
+    int l, first, live;
     uint32_t em[KV];
-    __device__ Cols(int lane, int W_, int first_, int N)
-        : l(lane), W(W_), first(kEdge ? first_ : 0)
+    __device__ Cols(int lane, int first_, int N) : l(lane), first(kEdge ? first_ : 0), live(0)
     {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
             const int c = col(j), lo = c < 0 ? -c : 0, hi = N - c < VEC ? N - c : VEC;
             em[j] = hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+            if (KV == 1 || c - (l & 31) * VEC < N) live = j + 1;
         }
     }
     __device__ int vec(int j) const { return l + j * W; }
@@ -377,8 +379,9 @@ struct Cols {
 
 // Weights of a thread's vectors as float32 (1 + w for Gemma), zeros outside
 // the row.  Whole vectors of an aligned weight come as 16-byte loads.
-template <int VEC, int KV, bool kEdge>
-__device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2], const Cols<VEC, KV, kEdge>& c,
+template <int VEC, int W, int KV, bool kEdge>
+__device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2],
+                                             const Cols<VEC, W, KV, kEdge>& c,
                                              const void* w, int wt, bool gemma)
 {
     constexpr int P = VEC / 2;
@@ -424,16 +427,15 @@ __device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2], const Cols<V
         }
 }
 
-// Sums (and NaN-keeping maxima) over a row group, U rows at once: every
-// thread of a group gets the same bits.  kW > 0: a group is kW <= 32 lanes of
-// a warp.  kW 0: a group of up to kWarps whole warps, joined through `red`
-// (row_red_floats, zero where no warp writes) with one __syncthreads; the two
-// halves of red are used in turn.
-template <int kW, int kWarps, int G, int U, bool kMax>
+// Sums (and NaN-keeping maxima) over the W threads of a row group, U rows at
+// once: every thread of a group gets the same bits.  Groups of several warps
+// join through `red` (row_red_floats) with one __syncthreads; its two halves
+// are used in turn.
+template <int W, int T, int U, bool kMax>
 __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* red, int& parity,
                                            int g, int l)
 {
-    constexpr int kIn = kW ? kW : 32;
+    constexpr int kIn = W < 32 ? W : 32;
     butterfly<kIn, U>(s);
     if constexpr (kMax) {
 #pragma unroll
@@ -442,8 +444,8 @@ __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* 
             for (int u = 0; u < U; ++u)
                 m[u] = max_nan(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
     }
-    if constexpr (kW == 0) {
-        constexpr int kV = kMax ? 2 * U : U;
+    if constexpr (W > 32) {
+        constexpr int kWarps = W / 32, G = T / W, kV = kMax ? 2 * U : U;
         const int lane = threadIdx.x & 31;
         float* slot = red + (parity * G + g) * kV * kWarps;
         if (lane == 0) {
@@ -470,16 +472,10 @@ __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* 
         parity ^= 1;
     }
 }
-template <int kW, int kWarps, int G, int U, bool kMax>
+template <int W, int T, int U, bool kMax>
 constexpr int row_red_floats()
 {
-    return kW ? 1 : 2 * G * (kMax ? 2 * U : U) * kWarps;
-}
-// Zero red; the caller's next __syncthreads publishes it.
-template <int kFloats>
-__device__ __forceinline__ void row_red_init(float* red)
-{
-    for (int i = threadIdx.x; i < kFloats; i += blockDim.x) red[i] = 0.f;
+    return W > 32 ? 2 * (T / W) * (kMax ? 2 * U : U) * (W / 32) : 1;
 }
 
 // Largest magnitude of a vector's elements, NaN on top, from its packed form:

@@ -61,32 +61,60 @@ gbn::Q8 q8_of(void* v, const float* scale, int type, int64_t N, int64_t group)
     return q;
 }
 
+// Whether groups fitted to the row pay (four vectors a thread, kRowFit): where
+// a fixed group's second half is nearly empty.  Measured, bf16, 2^26 elements:
+// forward N = 4097 131 -> 98 us and N = 2050 133 -> 117, but N = 5120 (5/8
+// full) 85 -> 94; backward N = 5120 113 -> 97, N = 4097 228 -> 176, but
+// N = 3001 (0.73 full) 146 -> 175; from a checkpoint N = 2050 271 -> 372.
+bool fit_pays(int kind, bool packed, int64_t nvec, int64_t cap)
+{
+    return kind != gbn::kKindB ? 16 * nvec <= 9 * cap : !packed && 8 * nvec <= 5 * cap;
+}
+
 // The vectors a row of N elements may touch: one more than N / VEC where rows
 // start inside a vector; and the first schedule that holds them (-1: none).
 int64_t row_vectors(int64_t N, int vec, bool edge)
 {
     return edge ? (N + 2 * vec - 2) / vec : N / vec;
 }
-int find_sched(int64_t nvec)
+int find_sched(int kind, bool packed, int64_t nvec)
 {
-    for (int s = 0; s < gbn::kNumRowSched; ++s)
-        if (nvec <= gbn::row_sched(false, s).cap) return s;
+    for (int s = 0; s < gbn::kRowFit; ++s) {
+        const gbn::RowSched& e = gbn::row_sched(kind, s);
+        if (nvec > e.cap) continue;
+        return nvec > 128 && nvec <= gbn::row_sched(kind, gbn::kRowFit).cap &&
+                       fit_pays(kind, packed, nvec, e.cap)
+                   ? gbn::kRowFit
+                   : s;
+    }
     return -1;
 }
 
-// CTAs the device holds at once.
-int64_t row_ctas(int sid, bool bwd, bool edge, int sms)
+// The launch's threads per row group, groups and CTAs on the device.
+struct RowShape {
+    int W, G, R;
+    int64_t ctas;
+};
+RowShape row_shape(int kind, int sid, int64_t nvec, bool edge, int sms)
 {
-    const int64_t ctas = (int64_t)sms * (bwd ? gbn::bwd_minb(sid) : gbn::fwd_minb(sid, edge));
+    const gbn::RowSched& e = gbn::row_sched(kind, sid);
+    RowShape s;
+    s.W = e.W ? e.W : (int)((nvec + 32 * e.KV - 1) / (32 * e.KV)) * 32;
+    s.G = gbn::row_G(kind, sid, s.W);
+    s.R = s.G * gbn::row_U(kind, sid);
+    const int minb = gbn::row_minb(kind, sid, edge);
+    // a CTA below its launch bound's size: as many as the same registers hold
+    s.ctas = (int64_t)sms * (minb * e.T / (s.W * s.G));
     // rows that start inside a vector need CTAs to step by a multiple of VEC rows
-    return ctas >= 8 ? ctas / 8 * 8 : ctas;
+    if (s.ctas >= 8) s.ctas = s.ctas / 8 * 8;
+    return s;
 }
 
 // The ring kernel's launch, or false where the general kernel takes the call:
 // every tensor on a 16-byte boundary, scattered rows whole vectors on such
 // boundaries, and a schedule for the width.  groups: the scales per row that
 // the kernel finds (0: none).
-bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const RowSrc* in, int nt,
+bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const RowSrc* in, int nt,
                std::initializer_list<const void*> outs, int groups, int sms)
 {
     const int vec = 16 / elem_bytes(xt);
@@ -100,11 +128,13 @@ bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const Ro
             return false;
     }
     const int64_t nvec = row_vectors(N, vec, p.edge);
-    p.sid = find_sched(nvec);
+    p.sid = find_sched(kind, in[0].row_bytes == N && kind == gbn::kKindB, nvec);
     if (p.sid < 0) return false;
-    const gbn::RowSched& e = gbn::row_sched(bwd, p.sid);
-    p.R = gbn::row_R(bwd, p.sid);
-    p.stages = bwd ? gbn::bwd_stages(p.sid) : gbn::fwd_stages(p.sid);
+    const RowShape sh = row_shape(kind, p.sid, nvec, p.edge, sms);
+    p.W = sh.W;
+    p.G = sh.G;
+    p.R = sh.R;
+    p.stages = gbn::row_stages(kind, p.sid);
     uint32_t at = 0;
     p.plain = 1;
     for (int t = 0; t < nt; ++t) {
@@ -117,12 +147,13 @@ bool plan_rows(gbn::RowPlan& p, bool bwd, int xt, int64_t M, int64_t N, const Ro
     p.stage_bytes = at;
     p.gm_off = 128 + p.stages * at;
     p.smem = p.gm_off + (p.edge && groups > 1 ? 2 * (size_t)p.R * groups * sizeof(float) : 0);
-    if (bwd) {  // the CTA's column sums take the drained ring
-        const size_t cols = 128 + (size_t)e.T * e.KV * vec * sizeof(float);
+    if (kind == gbn::kKindB) {  // the CTA's column sums take the drained ring
+        const size_t cols = 128 + (size_t)p.W * p.G * gbn::row_sched(kind, p.sid).KV * vec *
+                                  sizeof(float);
         p.smem = p.smem > cols ? p.smem : cols;
     }
     p.nblocks = (M + p.R - 1) / p.R;
-    const int64_t cap = row_ctas(p.sid, bwd, p.edge, sms);
+    const int64_t cap = sh.ctas;
     p.grid = (int)(p.nblocks < cap ? p.nblocks : cap);
     if (p.edge && p.nblocks > cap && cap * p.R % vec != 0) return false;
     return p.smem <= (size_t)gbn::kMaxSmem;
@@ -167,12 +198,14 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     a.inv_n = (float)(1.0 / (double)N);
     a.wt = f.wt;
     a.variant = f.variant;
-    gbn::RowPlan p;
     const gbn::Q8& q8 = f.q.v ? f.q : f.c;
-    if (!plan_rows(p, false, f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))
+    const int mode =
+        (!f.w ? gbn::kModeC : f.q.v ? gbn::kModeQ : f.c.v ? gbn::kModeYC : gbn::kModeY) +
+        (q8.v && q8.type == gbn::kInt8 ? gbn::kModeInt8 : 0);
+    gbn::RowPlan p;
+    if (!plan_rows(p, gbn::fwd_kind(mode), f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))
         return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));
     if (!(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
-    const int mode = !f.w ? gbn::kModeC : f.q.v ? gbn::kModeQ : f.c.v ? gbn::kModeYC : gbn::kModeY;
     return launch_status(f.xt == gbn::kF32   ? gbn::launch_add_fwd_f32(stream, mode, a, p)
                          : f.xt == gbn::kF16 ? gbn::launch_add_fwd_f16(stream, mode, a, p)
                                              : gbn::launch_add_fwd_bf16(stream, mode, a, p));
@@ -210,7 +243,7 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     if (sms <= 0) return GBN_EDEVICE;
     if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
     gbn::RowPlan p{};
-    const bool fast = M > 0 && plan_rows(p, true, xt, M, N, a.in, 3, {dx}, 0, sms);
+    const bool fast = M > 0 && plan_rows(p, gbn::kKindB, xt, M, N, a.in, 3, {dx}, 0, sms);
     if (fast && !(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
     const int64_t P = M == 0 ? 0 : fast ? p.grid : gbn::add_bwd_general_rows(M, N, sms);
     if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
@@ -225,7 +258,7 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     a.wt = wt;
     a.variant = variant;
     if (M > 0) {
-        const int mode = cscale                           ? gbn::kBwdC
+        const int mode = cscale ? (ct == gbn::kInt8 ? gbn::kBwdInt8 : gbn::kBwdC)
                          : variant == GBN_RMS_CAST_FIRST ? gbn::kBwdCast
                                                          : gbn::kBwdS;
         const cudaError_t rc = !fast               ? gbn::launch_add_bwd_general(stream, xt, P, a)
@@ -247,12 +280,12 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
     const int vec = 16 / elem_bytes(xt);
     const bool edge = N % vec != 0;
     const int64_t nvec = row_vectors(N, vec, edge);
-    const int sid = find_sched(nvec);
     int64_t P = add_bwd_general_rows(M, N, sms);
-    if (sid >= 0) {
-        const int64_t R = row_R(true, sid), blocks = (M + R - 1) / R;
-        const int64_t cap = row_ctas(sid, true, edge, sms);
-        const int64_t grid = blocks < cap ? blocks : cap;
+    for (const bool packed : {false, true}) {
+        const int sid = find_sched(kKindB, packed, nvec);
+        if (sid < 0) continue;
+        const RowShape sh = row_shape(kKindB, sid, nvec, edge, sms);
+        const int64_t blocks = (M + sh.R - 1) / sh.R, grid = blocks < sh.ctas ? blocks : sh.ctas;
         P = P > grid ? P : grid;
     }
     const size_t need = (size_t)P * (size_t)N * sizeof(float);

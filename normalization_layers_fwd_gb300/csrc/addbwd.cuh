@@ -9,26 +9,31 @@ namespace gbn {
 namespace {
 
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
+__global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
     add_bwd_ring(const __grid_constant__ BwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int W = kRowB[S].W, T = kRowB[S].T, KV = kRowB[S].KV, G = row_G(true, S);
-    constexpr int U = row_U(true, S), R = row_R(true, S);
+    constexpr int kW = kRowB[S].W, KV = kRowB[S].KV, U = row_U(kKindB, S);
+    constexpr int kG = row_G(kKindB, S), kLanes = kW ? kW : 256;
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
-    constexpr bool kPacked = kMode == kBwdC, kCast = kMode == kBwdCast, kLean = KV > 2;
+    constexpr bool kPacked = kMode >= kBwdC, kCast = kMode == kBwdCast, kLean = KV > 2;
+    constexpr int kType = kMode == kBwdInt8 ? kInt8 : kE4M3;
     // words of a thread's vector of s: activations, or 8-bit codes
     constexpr int NS = kPacked ? VEC / 4 : 4, VS = kPacked ? VEC : 16, ES = kPacked ? 1 : E;
+    constexpr int kRed = row_red_floats<kLanes, kG, U, false>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[row_red_floats<W, T, U, false>()];
+    __shared__ float red[kRed];
     int parity = 0;
-    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
+    const int N = a.N, W = kW ? kW : pl.W, G = kW ? kG : pl.G, R = G * U;
+    const int g = threadIdx.x / W, l = threadIdx.x - g * W;
+    if constexpr (kW == 0)
+        for (int i = threadIdx.x; i < kRed; i += W * G) red[i] = 0.f;
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
 
     int64_t row = (int64_t)blockIdx.x * R + g;  // this thread's first row
-    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(row * N % VEC) : 0, N);
+    const Cols<VEC, kW, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P], acc[KV][P];
-    load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    load_weights<VEC, kW, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
 #pragma unroll
     for (int j = 0; j < KV; ++j)
 #pragma unroll
@@ -92,15 +97,15 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
             const bool ok = okr[u] && cols.ok(j);
             const uint32_t o = so0 + u * G * (uint32_t)a.in[0].row_bytes + j * W * VS;
             if constexpr (kPacked) {
-                ld_vec8<VEC, kEdge>(v, slot, sc0 + o, ok, cols.em[j]);
+                ld_vec8<VEC>(v, slot, sc0 + o, ok, cols.cut(j), cols.em[j]);
             } else {
-                const uint4 q = ld_vec<TX, kEdge>(slot, o, ok, cols.em[j]);
+                const uint4 q = ld_vec<TX>(slot, o, ok, cols.cut(j), cols.em[j]);
                 v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
             }
         };
         auto ld_act = [&](int u, int j, bool present, uint32_t so) {
             const uint32_t o = so + u * G * (uint32_t)a.in[1].row_bytes + j * W * 16;
-            return ld_vec<TX, kEdge>(slot, o, okr[u] && cols.ok(j) && present, cols.em[j]);
+            return ld_vec<TX>(slot, o, okr[u] && cols.ok(j) && present, cols.cut(j), cols.em[j]);
         };
         uint32_t sp[U][KV][NS];
         uint4 dyp[U][KV], dsp[U][KV];
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
             if constexpr (kPacked) {
 #pragma unroll
                 for (int i = 0; i < VEC / 4; ++i)
-                    q8_unpack4(sp[u][j][i], xh[2 * i], xh[2 * i + 1], a.c.type);
+                    q8_unpack4<kType>(sp[u][j][i], xh[2 * i], xh[2 * i + 1]);
                 if constexpr (kEdge) {
                     const int eb = whole ? VEC : ((group_of(j) + 1) << a.c.shift) - cols.col(j);
                     const float ka = sc[u][j][0], kb = sc[u][j][kSc - 1];
@@ -147,13 +152,19 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
                 if constexpr (kCast) dn[p] = round2<TX>(dn[p]);
             }
         };
+        // xhat and dn are kept over the reduction where they fit the registers
+        // (8-bit codes take few), and computed again elsewhere
+        constexpr bool kKeep = kPacked && !kEdge && !kLean;
+        f2 xk[kKeep ? U : 1][kKeep ? KV : 1][P], dk[kKeep ? U : 1][kKeep ? KV : 1][P];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             f2 q = splat2(0.f);
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
                 if (KV > 1 && j >= cols.live) continue;
-                f2 xh[P], dn[P], dv[P];
+                f2 (&xh)[P] = xk[kKeep ? u : 0][kKeep ? j : 0];
+                f2 (&dn)[P] = dk[kKeep ? u : 0][kKeep ? j : 0];
+                f2 dv[P];
                 terms(u, j, xh, dn, dv);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
             }
             sum[u] = lo2(q) + hi2(q);
         }
-        row_reduce<W, T, U, false>(sum, none, red, parity, g, l);
+        row_reduce<kLanes, kG, U, false>(sum, none, red, parity, g, l);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const f2 r2 = splat2(rs[u]), nm = splat2(-(sum[u] * a.inv_n));
@@ -179,28 +190,30 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
                 if (KV > 1 && j >= cols.live) continue;
-                f2 xh[P], dn[P], dv[P];
-                terms(u, j, xh, dn, dv);
+                f2 (&xh)[P] = xk[kKeep ? u : 0][kKeep ? j : 0];
+                f2 (&dn)[P] = dk[kKeep ? u : 0][kKeep ? j : 0];
+                f2 dv[P];
+                if constexpr (!kKeep) terms(u, j, xh, dn, dv);
                 if constexpr (kLean) dsp[u][j] = ld_act(u, j, a.in[2].p != nullptr, so2);
                 unpack2<TX>(dsp[u][j], dv);
 #pragma unroll
                 for (int p = 0; p < P; ++p) dv[p] = fma2(r2, fma2(xh[p], nm, dn[p]), dv[p]);
-                st_vec<TX, kEdge>(dxr + j * W * VEC, pack2<TX>(dv), okr[u] && cols.ok(j),
-                                  cols.em[j]);
+                st_vec<TX>(dxr + j * W * VEC, pack2<TX>(dv), okr[u] && cols.ok(j), cols.cut(j),
+                           cols.em[j]);
             }
         }
         row += row_step;
         at += at_step;
-        return W > 32 && !kLean;  // row_reduce's barrier came after the last slot read
+        return kLanes > 32 && !kLean;  // row_reduce's barrier came after the last slot read
     });
 
     if (a.ws == nullptr) return;  // no weight gradient wanted (uniform)
     // The CTA's column sums, its row groups added in order: each group leaves
     // its vectors in the drained ring, and column c of group q is found
     // `first` of that group's rows further on.
-    constexpr int cap = W * KV * VEC;
+    const int cap = W * KV * VEC;
     float* const out = a.ws + blockIdx.x * (int64_t)N;
-    if constexpr (G == 1) {
+    if (G == 1) {
 #pragma unroll
         for (int j = 0; j < KV; ++j)
 #pragma unroll
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(kRowB[S].T, bwd_minb(S))
                 *reinterpret_cast<float2*>(buf + g * cap + cols.vec(j) * VEC + 2 * p) =
                     make_float2(lo2(acc[j][p]), hi2(acc[j][p]));
         __syncthreads();
-        for (int c = threadIdx.x; c < N; c += T) {
+        for (int c = threadIdx.x; c < N; c += W * G) {
             float t = 0.f;
 #pragma unroll 4
             for (int q = 0; q < G; ++q) {
@@ -237,12 +250,14 @@ cudaError_t bwd_launch(cudaStream_t st, int mode, const BwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_bwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, kRowB[S].T, p.smem, st, a, p);
+        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;
         if (mode == kBwdC)
             go(s_, edge_, integral_constant<int, kBwdC>{});
+        else if (mode == kBwdInt8)
+            go(s_, edge_, integral_constant<int, kBwdInt8>{});
         else if (mode == kBwdCast && is16<TX>())
             go(s_, edge_, integral_constant<int, is16<TX>() ? kBwdCast : kBwdS>{});
         else

@@ -12,9 +12,9 @@ namespace gbn {
 namespace {
 
 // VEC values times k (ka before element eb, kb from it on) as 8-bit codes.
-template <int VEC, bool kTwo>
+template <int VEC, bool kTwo, int kType>
 __device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v)[VEC / 2],
-                                          float ka, float kb, int eb, int type)
+                                          float ka, float kb, int eb)
 {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
@@ -23,30 +23,35 @@ __device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v
             k0 = mk2(4 * i < eb ? ka : kb, 4 * i + 1 < eb ? ka : kb);
             k1 = mk2(4 * i + 2 < eb ? ka : kb, 4 * i + 3 < eb ? ka : kb);
         }
-        out[i] = q8_pack4(v[2 * i], v[2 * i + 1], k0, k1, type);
+        out[i] = q8_pack4<kType>(v[2 * i], v[2 * i + 1], k0, k1);
     }
 }
 
-template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
+template <typename TX, int S, bool kEdge, int kFull>
+__global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_kind(kFull), S, kEdge))
     add_fwd_ring(const __grid_constant__ FwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int W = kRowF[S].W, T = kRowF[S].T, KV = kRowF[S].KV, G = row_G(false, S);
-    constexpr int U = row_U(false, S), R = row_R(false, S);
+    constexpr int kMode = kFull & 3, kType = kFull >= kModeInt8 ? kInt8 : kE4M3;
+    constexpr int kKind = fwd_kind(kMode), kW = row_sched(kKind, S).W, KV = row_sched(kKind, S).KV;
+    constexpr int U = row_U(kKind, S), kG = row_G(kKind, S), kLanes = kW ? kW : 256;
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
     constexpr bool kNorm = kMode != kModeC, kMax = kMode != kModeY;
+    constexpr int kRed = row_red_floats<kLanes, kG, U, kMax>();
     extern __shared__ __align__(128) unsigned char dsm[];
-    __shared__ float red[row_red_floats<W, T, U, kMax>()];
+    __shared__ float red[kRed];
     int parity = 0;
-    const int N = a.N, g = threadIdx.x / W, l = threadIdx.x % W;
+    const int N = a.N, W = kW ? kW : pl.W, G = kW ? kG : pl.G, R = G * U;
+    const int g = threadIdx.x / W, l = threadIdx.x - g * W;
+    if constexpr (kW == 0)
+        for (int i = threadIdx.x; i < kRed; i += W * G) red[i] = 0.f;
     const int64_t K = row_ring_start(a.in, pl, a.M, dsm);
 
     // the first row of this thread; its later ones are a multiple of VEC rows on
     int64_t row = (int64_t)blockIdx.x * R + g;
-    const Cols<VEC, W, KV, kEdge> cols(l, kEdge ? (int)(row * N % VEC) : 0, N);
+    const Cols<VEC, kW, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P];
-    if constexpr (kNorm) load_weights<VEC, W, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    if constexpr (kNorm) load_weights<VEC, kW, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
     // this thread's first vector: its element in the [M, N] tensors, and its
     // byte in a slot (rows of a slot are row_bytes apart)
     int64_t at = row * N - cols.first + l * VEC;
@@ -62,6 +67,8 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
     // kEdge: a vector's elements before eb belong to group ga, the others to the next
     int ga[KV], eb[KV];
     bool lead[KV];  // the vector holds its group's first column
+    constexpr int kIn = kLanes < 32 ? kLanes : 32;
+    const int shift = kEdge && cols.first != 0 ? 1 : 0;
     float* const gm = reinterpret_cast<float*>(dsm + pl.gm_off);  // [2][R][ng] maxima (kEdge)
     const bool shared_max = kEdge && kMax && !whole;
     if constexpr (kMax) {
@@ -73,7 +80,7 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
             lead[j] = cols.ok(j) && (c & (whole ? -1 : (1 << q8.shift) - 1)) == 0;
         }
         if (shared_max) {
-            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += T) gm[i] = 0.f;
+            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += W * G) gm[i] = 0.f;
             __syncthreads();
         }
     }
@@ -97,16 +104,18 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
                 if (KV > 1 && j >= cols.live) continue;
                 const bool ok = okr[u] && cols.ok(j);
                 const uint32_t o = u * srow + j * W * 16;
-                sp[u][j] = ld_vec<TX, kEdge>(slot, so0 + o, ok, cols.em[j]);
+                sp[u][j] = ld_vec<TX>(slot, so0 + o, ok, cols.cut(j), cols.em[j]);
                 if (a.in[1].p) {
-                    const uint4 rv = ld_vec<TX, kEdge>(slot, so1 + o, ok, cols.em[j]);
+                    const uint4 rv =
+                        ld_vec<TX>(slot, so1 + o, ok, cols.cut(j), cols.em[j]);
                     f2 xa[P], xb[P];
                     unpack2<TX>(sp[u][j], xa);
                     unpack2<TX>(rv, xb);
 #pragma unroll
                     for (int p = 0; p < P; ++p) xa[p] = add2(xa[p], xb[p]);
                     sp[u][j] = pack2<TX>(xa);  // the stream, rounded once
-                    if (a.s) st_vec<TX, kEdge>(sr + j * W * VEC, sp[u][j], ok, cols.em[j]);
+                    if (a.s)
+                        st_vec<TX>(sr + j * W * VEC, sp[u][j], ok, cols.cut(j), cols.em[j]);
                 }
                 f2 sv[P];
                 unpack2<TX>(sp[u][j], sv);
@@ -132,8 +141,9 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
                         }
                         gmx[u][j] = m;
                         mx[u] = max_nan(mx[u], m);
-                    } else if (ok) {
-                        // both groups' shares; magnitudes compare like their bits (NaN on top)
+                    } else {
+                        // both groups' shares; the second goes to the next lane,
+                        // whose vector starts in that group
                         float ma = 0.f, mb = 0.f;
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
@@ -141,17 +151,33 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
                             if (2 * p < eb[j]) ma = max_nan(ma, lo); else mb = max_nan(mb, lo);
                             if (2 * p + 1 < eb[j]) ma = max_nan(ma, hi); else mb = max_nan(mb, hi);
                         }
-                        int* const m = reinterpret_cast<int*>(gm) +
-                                       (half * R + g + u * G) * q8.ng + ga[j];
-                        atomicMax(m, __float_as_int(ma));
-                        if (eb[j] < VEC && ga[j] + 1 < q8.ng) atomicMax(m + 1, __float_as_int(mb));
+                        const bool two = ok && eb[j] < VEC && ga[j] + 1 < q8.ng;
+                        const float up = __shfl_up_sync(0xffffffffu, two ? mb : 0.f, 1, kIn);
+                        if ((l & (kIn - 1)) != 0) ma = max_nan(ma, up);
+                        // the lanes of a warp that share a group: aligned runs of
+                        // `lanes`, one lane further on where rows start inside a
+                        // vector (lane 0 then ends a run of the warp before and
+                        // stays out).  Magnitudes compare like their bits (NaN on
+                        // top): one atomic a run, whose order does not matter
+                        const bool out = shift && (l & (kIn - 1)) == 0;
+                        float m = out ? 0.f : ma;
+                        for (int off = 1; off < lanes; off <<= 1)
+                            m = max_nan(m, __shfl_sync(0xffffffffu, m,
+                                                       ((((l - shift) & (kIn - 1)) ^ off) + shift) & (kIn - 1), kIn));
+                        unsigned* const dst = reinterpret_cast<unsigned*>(gm) +
+                                              (half * R + g + u * G) * q8.ng + ga[j];
+                        if (ok && (out || ((l - shift) & (lanes - 1)) == 0))
+                            atomicMax(dst, __float_as_uint(out ? ma : m));
+                        if (two && ((l & (kIn - 1)) == kIn - 1 ||
+                                    cols.col(j) + VEC >= N))  // no next lane to take it
+                            atomicMax(dst + 1, __float_as_uint(mb));
                     }
                 }
             }
         }
         // the row's sum, and its maximum for a scale per row; a group's
         // maximum from its lanes, or from shared memory
-        if (kNorm || whole) row_reduce<W, T, U, kMax>(ss, mx, red, parity, g, l);
+        if (kNorm || whole) row_reduce<kLanes, kG, U, kMax>(ss, mx, red, parity, g, l);
         if constexpr (kMax) {
             if (shared_max) {
                 __syncthreads();
@@ -188,8 +214,8 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
 #pragma unroll
                         for (int p = 0; p < P; ++p) o[p] = mul2(wf[j][p], mul2(sv[p], r2));
                     }
-                    st_vec<TX, kEdge>(static_cast<TX*>(a.y) + atu + j * W * VEC, pack2<TX>(o), ok,
-                                      cols.em[j]);
+                    st_vec<TX>(static_cast<TX*>(a.y) + atu + j * W * VEC, pack2<TX>(o), ok,
+                               cols.cut(j), cols.em[j]);
                 }
                 if constexpr (kMax) {
                     float ma = whole ? mx[u] : gmx[u][j], mb = 0.f;
@@ -203,17 +229,17 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
                         for (int p = 0; p < P; ++p) sv[p] = mul2(sv[p], wf[j][p]);
                     }
                     const float t = kMode == kModeQ ? rs : 1.f;  // r enters here
-                    const float sa = q8_scale(ma * t, q8.type);
+                    const float sa = q8_scale(ma * t, kType);
                     const float ka = t * __frcp_rn(sa);
                     float sb = 0.f, kb = ka;
                     if (shared_max) {
-                        sb = q8_scale(mb * t, q8.type);
+                        sb = q8_scale(mb * t, kType);
                         kb = t * __frcp_rn(sb);
                     }
                     uint32_t o[VEC / 4];
-                    pack_vec8<VEC, kEdge>(o, sv, ka, kb, eb[j], q8.type);
-                    st_vec8<VEC, kEdge>(static_cast<unsigned char*>(q8.v) + atu + j * W * VEC, o,
-                                        ok, cols.em[j]);
+                    pack_vec8<VEC, kEdge, kType>(o, sv, ka, kb, eb[j]);
+                    st_vec8<VEC>(static_cast<unsigned char*>(q8.v) + atu + j * W * VEC, o, ok,
+                                 cols.cut(j), cols.em[j]);
                     // the vector that holds a group's first column writes its scale
                     float* const sc = q8.scale + r * q8.ng + ga[j];
                     if (okr[u] && lead[j]) sc[0] = sa;
@@ -226,10 +252,10 @@ __global__ void __launch_bounds__(kRowF[S].T, fwd_minb(S, kEdge))
         if (shared_max) {
             // the other half is free: its readers passed the barrier above
             half ^= 1;
-            for (int i = threadIdx.x; i < R * q8.ng; i += T) gm[half * R * q8.ng + i] = 0.f;
+            for (int i = threadIdx.x; i < R * q8.ng; i += W * G) gm[half * R * q8.ng + i] = 0.f;
             return false;  // and a barrier before its next use
         }
-        return W > 32 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
+        return kLanes > 32 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
     });
 }
 
@@ -240,7 +266,7 @@ cudaError_t fwd_launch(cudaStream_t st, int mode, const FwdArgs& a, const RowPla
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
         ring_attributes<add_fwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, kRowF[S].T, p.smem, st, a, p);
+        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;
@@ -248,6 +274,15 @@ cudaError_t fwd_launch(cudaStream_t st, int mode, const FwdArgs& a, const RowPla
             case kModeY: go(s_, edge_, integral_constant<int, kModeY>{}); break;
             case kModeQ: go(s_, edge_, integral_constant<int, kModeQ>{}); break;
             case kModeYC: go(s_, edge_, integral_constant<int, kModeYC>{}); break;
+            case kModeQ + kModeInt8:
+                go(s_, edge_, integral_constant<int, kModeQ + kModeInt8>{});
+                break;
+            case kModeYC + kModeInt8:
+                go(s_, edge_, integral_constant<int, kModeYC + kModeInt8>{});
+                break;
+            case kModeC + kModeInt8:
+                go(s_, edge_, integral_constant<int, kModeC + kModeInt8>{});
+                break;
             default: go(s_, edge_, integral_constant<int, kModeC>{}); break;
         }
     };

@@ -74,6 +74,7 @@ struct UnpackArgs {
 // of every input at off[t].
 struct RowPlan {
     int sid, edge, grid;
+    int W, G;              // threads of a row group, row groups of a CTA
     int plain;             // every input's rows in order, of whole 16-byte units
     uint32_t block_bytes;  // of a whole block, all inputs
     int64_t nblocks;
@@ -84,8 +85,9 @@ struct RowPlan {
 };
 
 // One instance set per activation type (addfwd_*.cu, addbwd_*.cu).
-enum FwdMode : int { kModeY = 0, kModeQ = 1, kModeYC = 2, kModeC = 3 };
-enum BwdMode : int { kBwdS = 0, kBwdCast = 1, kBwdC = 2 };
+// The 8-bit modes come once per 8-bit type: + kModeInt8.
+enum FwdMode : int { kModeY = 0, kModeQ = 1, kModeYC = 2, kModeC = 3, kModeInt8 = 4 };
+enum BwdMode : int { kBwdS = 0, kBwdCast = 1, kBwdC = 2, kBwdInt8 = 3 };
 cudaError_t launch_add_fwd_bf16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_fwd_f16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_fwd_f32(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
@@ -126,9 +128,10 @@ __device__ __forceinline__ float q8_scale(float a, int type)
 // of floats there is 1); the product is rounded before it, in instructions
 // that may not be fused (ptxas 13.0 did fuse mul.rn.f32x2 with
 // add.rn.f32x2, and products next to a half went the other way).
-__device__ __forceinline__ uint32_t q8_pack4(f2 a, f2 b, f2 ka, f2 kb, int type)
+template <int kType>
+__device__ __forceinline__ uint32_t q8_pack4(f2 a, f2 b, f2 ka, f2 kb)
 {
-    if (type == kE4M3) {
+    if constexpr (kType == kE4M3) {
         a = mul2(a, ka);
         b = mul2(b, kb);
         uint32_t r;
@@ -139,20 +142,23 @@ __device__ __forceinline__ uint32_t q8_pack4(f2 a, f2 b, f2 ka, f2 kb, int type)
             : "=r"(r)
             : "f"(lo2(a)), "f"(hi2(a)), "f"(lo2(b)), "f"(hi2(b)));
         return r;
+    } else {
+        auto code = [](float v, float k) {
+            return __float_as_uint(__fadd_rn(__fmul_rn(v, k), 12582912.f));
+        };
+        return __byte_perm(__byte_perm(code(lo2(a), lo2(ka)), code(hi2(a), hi2(ka)), 0x0040),
+                           __byte_perm(code(lo2(b), lo2(kb)), code(hi2(b), hi2(kb)), 0x0040),
+                           0x5410);
     }
-    auto code = [](float v, float k) {
-        return __float_as_uint(__fadd_rn(__fmul_rn(v, k), 12582912.f));
-    };
-    return __byte_perm(__byte_perm(code(lo2(a), lo2(ka)), code(hi2(a), hi2(ka)), 0x0040),
-                       __byte_perm(code(lo2(b), lo2(kb)), code(hi2(b), hi2(kb)), 0x0040), 0x5410);
 }
 
 // Four 8-bit codes as floats, exactly.  e4m3 values are f16 values.  int8: a
 // byte with its sign bit turned, under the exponent of 2^23, is 2^23 + 128 +
 // its value.
-__device__ __forceinline__ void q8_unpack4(uint32_t w, f2& a, f2& b, int type)
+template <int kType>
+__device__ __forceinline__ void q8_unpack4(uint32_t w, f2& a, f2& b)
 {
-    if (type == kE4M3) {
+    if constexpr (kType == kE4M3) {
         uint32_t l, h;
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
             "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
@@ -161,25 +167,29 @@ __device__ __forceinline__ void q8_unpack4(uint32_t w, f2& a, f2& b, int type)
             : "r"(w));
         a = h2_to_f2(l);
         b = h2_to_f2(h);
-        return;
+    } else {
+        const uint32_t t = w ^ 0x80808080u, e = 0x4b000000u;
+        const f2 m = splat2(-8388736.f);  // -(2^23 + 128)
+        a = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7440)),
+                     __uint_as_float(__byte_perm(t, e, 0x7441))), m);
+        b = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7442)),
+                     __uint_as_float(__byte_perm(t, e, 0x7443))), m);
     }
-    const uint32_t t = w ^ 0x80808080u, e = 0x4b000000u;
-    const f2 m = splat2(-8388736.f);  // -(2^23 + 128)
-    a = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7440)),
-                 __uint_as_float(__byte_perm(t, e, 0x7441))), m);
-    b = add2(mk2(__uint_as_float(__byte_perm(t, e, 0x7442)),
-                 __uint_as_float(__byte_perm(t, e, 0x7443))), m);
 }
 
 // One value (the general kernels).
 __device__ __forceinline__ uint32_t q8_pack1(float v, float k, int type)
 {
-    return q8_pack4(mk2(v, 0.f), splat2(0.f), splat2(k), splat2(0.f), type) & 0xffu;
+    const f2 a = mk2(v, 0.f), z = splat2(0.f), kk = splat2(k);
+    return (type == kE4M3 ? q8_pack4<kE4M3>(a, z, kk, z) : q8_pack4<kInt8>(a, z, kk, z)) & 0xffu;
 }
 __device__ __forceinline__ float q8_unpack1(uint32_t b, int type)
 {
     f2 v, unused;
-    q8_unpack4(b, v, unused, type);
+    if (type == kE4M3)
+        q8_unpack4<kE4M3>(b, v, unused);
+    else
+        q8_unpack4<kInt8>(b, v, unused);
     return lo2(v);
 }
 

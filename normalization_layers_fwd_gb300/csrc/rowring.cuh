@@ -32,48 +32,63 @@ namespace gbn {
 // weight of every element next to the row.  The widest backward holds four
 // column sums and weights and reads its row from the ring a second time
 // instead of keeping it.  A warp skips those of its KV vectors that lie past
-// the row's end.
+// the row's end.  Rows that leave many lanes of a fixed group idle (kRowFit)
+// take groups of as many warps as they fill, with four vectors a thread.
 struct RowSched {
-    int cap, W, KV, T;
+    int cap, W, KV, T;  // W 0: kRowFit, chosen in the launch
 };
-constexpr int kNumRowSched = 10;
+constexpr int kNumRowSched = 11, kRowFit = 10;
 constexpr RowSched kRowF[kNumRowSched] = {
     {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
     {64, 32, 2, 256},  {128, 32, 4, 256}, {256, 64, 4, 256},  {512, 128, 4, 256},
-    {1024, 256, 4, 256}, {2048, 512, 4, 512},
+    {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
 };
 constexpr RowSched kRowB[kNumRowSched] = {
     {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
     {64, 32, 2, 256},  {128, 64, 2, 256}, {256, 128, 2, 256}, {512, 256, 2, 256},
-    {1024, 512, 2, 512}, {2048, 512, 4, 512},
+    {1024, 512, 2, 512}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
 };
-constexpr const RowSched& row_sched(bool bwd, int S) { return bwd ? kRowB[S] : kRowF[S]; }
-constexpr int row_G(bool bwd, int S) { return row_sched(bwd, S).T / row_sched(bwd, S).W; }
+// The forward that also packs the checkpoint does the most per element; two
+// vectors a thread leave it three CTAs an SM ([16384, 4096] bf16: 99 us, 108
+// with four vectors and two CTAs).
+constexpr RowSched kRowC[kNumRowSched] = {
+    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
+    {64, 32, 2, 256},  {128, 64, 2, 256}, {256, 128, 2, 256}, {512, 256, 2, 256},
+    {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
+};
+enum RowKind : int { kKindF = 0, kKindC = 1, kKindB = 2, kKindQ = 3 };
+constexpr int fwd_kind(int mode)
+{
+    return (mode & 3) == kModeYC ? kKindC : (mode & 3) == kModeQ ? kKindQ : kKindF;
+}
+constexpr const RowSched& row_sched(int kind, int S)
+{
+    return kind == kKindB ? kRowB[S] : kind == kKindC ? kRowC[S] : kRowF[S];
+}
+// Row groups of a CTA (kRowFit: with W threads each).
+constexpr int row_G(int kind, int S, int W = 0)
+{
+    const RowSched& e = row_sched(kind, S);
+    return e.W ? e.T / e.W : W <= 64 ? 4 : W <= 128 ? 2 : 1;
+}
 // Rows a thread takes of a block: two of one vector.  (A thread's rows of a
 // block are G apart, a multiple of VEC: rows that start inside a vector keep
 // one mask and one set of weights a thread.)
-constexpr int row_U(bool bwd, int S) { return row_sched(bwd, S).KV == 1 ? 2 : 1; }
-constexpr int row_R(bool bwd, int S) { return row_G(bwd, S) * row_U(bwd, S); }
+constexpr int row_U(int kind, int S) { return row_sched(kind, S).KV == 1 ? 2 : 1; }
 // CTAs an SM holds at least (their register budget), and ring stages.
-#ifndef GBN_FMINB1
-#define GBN_FMINB1 4
-#endif
-#ifndef GBN_FST1
-#define GBN_FST1 2
-#endif
-#ifndef GBN_FST
-#define GBN_FST 2
-#endif
-#ifndef GBN_BST
-#define GBN_BST 3
-#endif
-constexpr int fwd_minb(int S, bool edge)
+constexpr int row_minb(int kind, int S, bool edge)
 {
-    return kRowF[S].T == 512 ? 1 : kRowF[S].KV > 1 ? 2 : edge ? 3 : GBN_FMINB1;
+    const RowSched& e = row_sched(kind, S);
+    return e.T == 512    ? 1
+           : kind == kKindB ? 2
+           : e.KV == 1      ? (edge ? 3 : 4)
+           : e.KV == 2 && kind != kKindF ? 3
+                                         : 2;
 }
-constexpr int bwd_minb(int S) { return kRowB[S].T == 512 ? 1 : 2; }
-constexpr int fwd_stages(int S) { return kRowF[S].KV == 1 ? GBN_FST1 : GBN_FST; }
-constexpr int bwd_stages(int S) { return kRowB[S].KV == 4 ? 2 : GBN_BST; }
+constexpr int row_stages(int kind, int S)
+{
+    return kind == kKindB && row_sched(kind, S).KV < 4 ? 3 : 2;
+}
 // Dynamic shared memory the kernels may ask for: three inputs of the widest
 // rows (32 KB each) in two stages, and room for the group maxima.
 constexpr int kMaxSmem = 208 * 1024;
@@ -257,42 +272,37 @@ __device__ __forceinline__ uint32_t lds32(const void* p)
     return v;
 }
 
-// A vector's words of NW words with the elements outside the mask zeroed;
-// Mask holds one word of bits per word.
+// The NW words of a vector with the elements outside the mask zeroed.
 template <int VEC, int NW>
-struct Mask {
-    uint32_t m[NW];
-    __device__ explicit Mask(uint32_t em)
-    {
-        constexpr int per = VEC / NW, bits = 32 / per;  // elements a word
+__device__ __forceinline__ void mask_words(uint32_t (&v)[NW], uint32_t em)
+{
+    constexpr int per = VEC / NW, bits = 32 / per;  // elements a word
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            m[i] = 0;
+    for (int i = 0; i < NW; ++i)
 #pragma unroll
-            for (int e = 0; e < per; ++e)
-                if ((em >> (i * per + e)) & 1u)
-                    m[i] |= (per == 1 ? ~0u : (1u << (bits % 32)) - 1u) << (e * bits % 32);
-        }
-    }
-};
+        for (int e = 0; e < per; ++e)
+            if (!((em >> (i * per + e)) & 1u))
+                v[i] &= per == 1 ? 0u : ~(((1u << (bits % 32)) - 1u) << (e * bits % 32));
+}
 
-// 16 bytes of activations at byte o of the slot; kEdge: masked.
-template <typename TX, bool kEdge>
-__device__ __forceinline__ uint4 ld_vec(const unsigned char* slot, uint32_t o, bool ok,
+// 16 bytes of activations at byte o of the slot; cut: masked.
+template <typename TX>
+__device__ __forceinline__ uint4 ld_vec(const unsigned char* slot, uint32_t o, bool ok, bool cut,
                                         uint32_t em)
 {
     uint4 v = lds128_if(ok, slot + o);
-    if constexpr (kEdge) {
-        const Mask<Vec<TX>::kN, 4> k(em);
-        v.x &= k.m[0], v.y &= k.m[1], v.z &= k.m[2], v.w &= k.m[3];
+    if (cut) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        mask_words<Vec<TX>::kN>(w, em);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return v;
 }
 
 // A vector's VEC 8-bit values.
-template <int VEC, bool kEdge>
+template <int VEC>
 __device__ __forceinline__ void ld_vec8(uint32_t (&v)[VEC / 4], const unsigned char* slot,
-                                        uint32_t o, bool ok, uint32_t em)
+                                        uint32_t o, bool ok, bool cut, uint32_t em)
 {
     if constexpr (VEC == 8) {
         const uint2 q = ok ? lds64(slot + o) : make_uint2(0, 0);
@@ -301,69 +311,58 @@ __device__ __forceinline__ void ld_vec8(uint32_t (&v)[VEC / 4], const unsigned c
     } else {
         v[0] = ok ? lds32(slot + o) : 0u;
     }
-    if constexpr (kEdge) {
-        const Mask<VEC, VEC / 4> k(em);
+    if (cut) mask_words<VEC>(v, em);
+}
+
+// Store a vector of activations; cut: the elements in the mask.
+template <typename TX>
+__device__ __forceinline__ void st_vec(TX* p, const uint4& v, bool ok, bool cut, uint32_t em)
+{
+    constexpr uint32_t kFull = (1u << Vec<TX>::kN) - 1u;
+    st_stream_if(ok && (!cut || em == kFull), p, v);
+    if (cut && ok && em != kFull) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) v[i] &= k.m[i];
+        for (int e = 0; e < Vec<TX>::kN; ++e)
+            if ((em >> e) & 1u) {
+                if constexpr (sizeof(TX) == 2)
+                    reinterpret_cast<unsigned short*>(p)[e] =
+                        (unsigned short)(w[e / 2] >> (16 * (e % 2)));
+                else
+                    reinterpret_cast<uint32_t*>(p)[e] = w[e];
+            }
     }
 }
 
-// Store a vector of activations: whole, or the elements in the mask.
-template <typename TX, bool kEdge>
-__device__ __forceinline__ void st_vec(TX* p, const uint4& v, bool ok, uint32_t em)
-{
-    if constexpr (kEdge) {
-        if (!ok) return;
-        if (em == (1u << Vec<TX>::kN) - 1u) {
-            st_stream(p, v);
-            return;
-        }
-        // by halves, an element a turn: little code for the one lane in many
-        uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
-        constexpr int kHalf = Vec<TX>::kN / 2, kBits = 64 / kHalf;
-        using W = typename std::conditional<sizeof(TX) == 2, unsigned short, uint32_t>::type;
-        W* const q = reinterpret_cast<W*>(p);
-#pragma unroll 1
-        for (int e = 0; e < kHalf; ++e) {
-            if ((em >> e) & 1u) q[e] = (W)lo;
-            if ((em >> (kHalf + e)) & 1u) q[kHalf + e] = (W)hi;
-            lo >>= kBits;
-            hi >>= kBits;
-        }
-    } else {
-        st_stream_if(ok, p, v);
-    }
-}
-
-template <int VEC, bool kEdge>
+template <int VEC>
 __device__ __forceinline__ void st_vec8(unsigned char* p, const uint32_t (&v)[VEC / 4], bool ok,
-                                        uint32_t em)
+                                        bool cut, uint32_t em)
 {
-    if (!ok) return;
-    if (kEdge && em != (1u << VEC) - 1u) {
-        uint64_t w = VEC == 8 ? (uint64_t)v[VEC / 4 - 1] << 32 | v[0] : v[0];
-#pragma unroll 1
-        for (int e = 0; e < VEC; ++e) {
-            if ((em >> e) & 1u) p[e] = (unsigned char)w;
-            w >>= 8;
-        }
-        return;
+    constexpr uint32_t kFull = (1u << VEC) - 1u;
+    if (ok && (!cut || em == kFull)) {
+        if constexpr (VEC == 8)
+            __stcs(reinterpret_cast<uint2*>(p), make_uint2(v[0], v[1]));
+        else
+            __stcs(reinterpret_cast<unsigned*>(p), v[0]);
     }
-    if constexpr (VEC == 8)
-        __stcs(reinterpret_cast<uint2*>(p), make_uint2(v[0], v[1]));
-    else
-        __stcs(reinterpret_cast<unsigned*>(p), v[0]);
+    if (cut && ok && em != kFull) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if ((em >> e) & 1u) p[e] = (unsigned char)(v[e / 4] >> (8 * (e % 4)));
+    }
 }
 
 // A thread's part of its rows: its vector j is vector l + j W of the row,
 // whose element 0 is column col(j) = (l + j W) VEC - first, and em[j] says
 // which of its elements are the row's.  The first `live` of them have a lane
 // of this warp in the row.
-template <int VEC, int W, int KV, bool kEdge>
+template <int VEC, int kW, int KV, bool kEdge>
 struct Cols {
-    int l, first, live;
+    int l, W, first, live;
     uint32_t em[KV];
-    __device__ Cols(int lane, int first_, int N) : l(lane), first(kEdge ? first_ : 0), live(0)
+    uint32_t partial;  // bit j: a lane of this warp holds part of a vector j (the same on all)
+    __device__ Cols(int lane, int W_, int first_, int N)
+        : l(lane), W(kW ? kW : W_), first(kEdge ? first_ : 0), live(0)
     {
 #pragma unroll
         for (int j = 0; j < KV; ++j) {
@@ -371,17 +370,27 @@ struct Cols {
             em[j] = hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
             if (KV == 1 || c - (l & 31) * VEC < N) live = j + 1;
         }
+        partial = 0;
+        if constexpr (kEdge) {
+#pragma unroll
+            for (int j = 0; j < KV; ++j)
+                if (__any_sync(0xffffffffu, em[j] != 0 && em[j] != (1u << VEC) - 1u))
+                    partial |= 1u << j;
+        }
     }
     __device__ int vec(int j) const { return l + j * W; }
     __device__ int col(int j) const { return vec(j) * VEC - first; }
     __device__ bool ok(int j) const { return em[j] != 0; }
+    // Whether vector j of some lane is partial: only then are loads masked and
+    // stores split (a warp-uniform branch).
+    __device__ bool cut(int j) const { return kEdge && ((partial >> j) & 1u); }
 };
 
 // Weights of a thread's vectors as float32 (1 + w for Gemma), zeros outside
 // the row.  Whole vectors of an aligned weight come as 16-byte loads.
-template <int VEC, int W, int KV, bool kEdge>
+template <int VEC, int kW, int KV, bool kEdge>
 __device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2],
-                                             const Cols<VEC, W, KV, kEdge>& c,
+                                             const Cols<VEC, kW, KV, kEdge>& c,
                                              const void* w, int wt, bool gemma)
 {
     constexpr int P = VEC / 2;
@@ -427,15 +436,16 @@ __device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2],
         }
 }
 
-// Sums (and NaN-keeping maxima) over the W threads of a row group, U rows at
-// once: every thread of a group gets the same bits.  Groups of several warps
-// join through `red` (row_red_floats) with one __syncthreads; its two halves
-// are used in turn.
-template <int W, int T, int U, bool kMax>
+// Sums (and NaN-keeping maxima) over the threads of a row group, U rows at
+// once: every thread of a group gets the same bits.  kLanes <= 32: a group is
+// kLanes lanes of a warp.  Otherwise it is up to kLanes / 32 whole warps,
+// joined through `red` (row_red_floats; zero where no warp writes) with one
+// __syncthreads; its two halves are used in turn.
+template <int kLanes, int G, int U, bool kMax>
 __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* red, int& parity,
                                            int g, int l)
 {
-    constexpr int kIn = W < 32 ? W : 32;
+    constexpr int kIn = kLanes < 32 ? kLanes : 32;
     butterfly<kIn, U>(s);
     if constexpr (kMax) {
 #pragma unroll
@@ -444,8 +454,8 @@ __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* 
             for (int u = 0; u < U; ++u)
                 m[u] = max_nan(m[u], __shfl_xor_sync(0xffffffffu, m[u], off));
     }
-    if constexpr (W > 32) {
-        constexpr int kWarps = W / 32, G = T / W, kV = kMax ? 2 * U : U;
+    if constexpr (kLanes > 32) {
+        constexpr int kWarps = kLanes / 32, kV = kMax ? 2 * U : U;
         const int lane = threadIdx.x & 31;
         float* slot = red + (parity * G + g) * kV * kWarps;
         if (lane == 0) {
@@ -472,10 +482,10 @@ __device__ __forceinline__ void row_reduce(float (&s)[U], float (&m)[U], float* 
         parity ^= 1;
     }
 }
-template <int W, int T, int U, bool kMax>
+template <int kLanes, int G, int U, bool kMax>
 constexpr int row_red_floats()
 {
-    return W > 32 ? 2 * (T / W) * (kMax ? 2 * U : U) * (W / 32) : 1;
+    return kLanes > 32 ? 2 * G * (kMax ? 2 * U : U) * (kLanes / 32) : 1;
 }
 
 // Largest magnitude of a vector's elements, NaN on top, from its packed form:
@@ -521,6 +531,7 @@ inline bool with_row_sched(int sid, F&& f)
         case 7: f(std::integral_constant<int, 7>{}); return true;
         case 8: f(std::integral_constant<int, 8>{}); return true;
         case 9: f(std::integral_constant<int, 9>{}); return true;
+        case 10: f(std::integral_constant<int, 10>{}); return true;
         default: return false;
     }
 }

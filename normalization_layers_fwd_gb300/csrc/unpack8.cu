@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kThreads = 256, kBatch = 4;
 
-template <typename TX>
+template <typename TX, int kType>
 __global__ void __launch_bounds__(kThreads)
     unpack_vec(const __grid_constant__ UnpackArgs a, int64_t step_rows, int step_cols)
 {
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads)
             f2 o[P];
 #pragma unroll
             for (int k = 0; k < VEC / 4; ++k)
-                q8_unpack4(w[i][k], o[2 * k], o[2 * k + 1], a.c.type);
+                q8_unpack4<kType>(w[i][k], o[2 * k], o[2 * k + 1]);
             const int end = cb[i] + VEC - 1;
             if (end < a.N && (end >> sh) == (cb[i] >> sh)) {
 #pragma unroll
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
     if (blockIdx.x == 0 && threadIdx.x < total - whole * VEC) {
         const int64_t i = whole * VEC + threadIdx.x, row = i / a.N;
         const float sc = a.c.scale[row * a.c.ng + ((int)(i - row * a.N) >> sh)];
-        st1(x, i, q8_unpack1(q[i], a.c.type) * sc);
+        st1(x, i, q8_unpack1(q[i], kType) * sc);
     }
 }
 
@@ -97,7 +97,13 @@ void unpack_launch(cudaStream_t st, int sms, const UnpackArgs& a)
     const int64_t ctas = (whole + per - 1) / per, cap = 8LL * sms;
     const int64_t grid = ctas < 1 ? 1 : ctas < cap ? ctas : cap;
     const int64_t step = grid * kThreads * VEC;
-    launch_pdl(unpack_vec<TX>, (unsigned)grid, kThreads, 0, st, a, step / a.N, (int)(step % a.N));
+    auto go = [&](auto kernel) {
+        launch_pdl(kernel, (unsigned)grid, kThreads, 0, st, a, step / a.N, (int)(step % a.N));
+    };
+    if (a.c.type == kE4M3)
+        go(unpack_vec<TX, kE4M3>);
+    else
+        go(unpack_vec<TX, kInt8>);
 }
 
 }  // namespace

@@ -25,7 +25,7 @@ LIB = os.path.join(OUT, "libgbnorm.so")
 
 SOURCES = ["add_api.cu", "addbwd_bf16.cu", "addbwd_f16.cu", "addbwd_f32.cu", "addfwd_bf16.cu",
            "addfwd_f16.cu", "addfwd_f32.cu", "addnorm.cu", "api.cu", "colsum.cu", "dyt.cu",
-           "layernorm.cu", "rmsnorm.cu", "rmsnorm_bwd.cu", "static_ws.cu", "unpack8.cu"]
+           "layernorm.cu", "pack8.cu", "rmsnorm.cu", "rmsnorm_bwd.cu", "static_ws.cu"]
 HEADERS = ["addbwd.cuh", "addfwd.cuh", "addnorm.cuh", "common.cuh", "ctx_cache.h", "internal.h",
            "rmsnorm.cuh", "rowring.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -136,17 +136,19 @@ bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const Ro
     p.R = sh.R;
     p.stages = gbn::row_stages(kind, p.sid);
     uint32_t at = 0;
-    p.plain = 1;
+    p.in_order = 1;
     for (int t = 0; t < nt; ++t) {
         p.off[t] = at;
         if (!in[t].p) continue;
-        if (in[t].scattered || in[t].row_bytes % 16 != 0) p.plain = 0;
-        p.block_bytes += (uint32_t)(p.R * in[t].row_bytes);
+        if (in[t].scattered)
+            p.in_order = 0;
+        else if (in[t].total % 16 != 0)
+            p.tail = 1;
         at += (uint32_t)(p.R * in[t].row_bytes + 32 + 127) / 128 * 128;
     }
     p.stage_bytes = at;
     p.gm_off = 128 + p.stages * at;
-    p.smem = p.gm_off + (p.edge && groups > 1 ? 2 * (size_t)p.R * groups * sizeof(float) : 0);
+    p.smem = p.gm_off + (p.edge && groups > 1 ? (size_t)p.R * (2 * groups + 1) * sizeof(float) : 0);
     if (kind == gbn::kKindB) {  // the CTA's column sums take the drained ring
         const size_t cols = 128 + (size_t)p.W * p.G * gbn::row_sched(kind, p.sid).KV * vec *
                                   sizeof(float);
@@ -202,6 +204,10 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     const int mode =
         (!f.w ? gbn::kModeC : f.q.v ? gbn::kModeQ : f.c.v ? gbn::kModeYC : gbn::kModeY) +
         (q8.v && q8.type == gbn::kInt8 ? gbn::kModeInt8 : 0);
+    // a checkpoint alone, of rows of whole groups, needs no row at all
+    if (!f.w && q8.shift != 31 && N % (1 << q8.shift) == 0 && !a.in[0].scattered &&
+        aligned(16, {f.x, q8.v}))
+        return launch_status(gbn::launch_pack_fast(stream, f.xt, sms, a));
     gbn::RowPlan p;
     if (!plan_rows(p, gbn::fwd_kind(mode), f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))
         return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));

@@ -11,20 +11,23 @@
 namespace gbn {
 namespace {
 
-// VEC values times k (ka before element eb, kb from it on) as 8-bit codes.
-template <int VEC, bool kTwo, int kType>
-__device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v)[VEC / 2],
-                                          float ka, float kb, int eb)
+// VEC values times k as 8-bit codes.
+template <int VEC, int kType>
+__device__ __forceinline__ void pack_vec8(uint32_t (&out)[VEC / 4], const f2 (&v)[VEC / 2], float k)
+{
+    const f2 kk = splat2(k);
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) out[i] = q8_pack4<kType>(v[2 * i], v[2 * i + 1], kk, kk);
+}
+
+// Bytes (of VEC / 4 words) or 16-bit halves (of VEC / 2) of the elements
+// before eb.
+template <int VEC, int NW>
+__device__ __forceinline__ void before(uint32_t (&m)[NW], int eb)
 {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-        f2 k0 = splat2(ka), k1 = k0;
-        if constexpr (kTwo) {
-            k0 = mk2(4 * i < eb ? ka : kb, 4 * i + 1 < eb ? ka : kb);
-            k1 = mk2(4 * i + 2 < eb ? ka : kb, 4 * i + 3 < eb ? ka : kb);
-        }
-        out[i] = q8_pack4<kType>(v[2 * i], v[2 * i + 1], k0, k1);
-    }
+    for (int i = 0; i < NW; ++i) m[i] = ~0u;
+    mask_words<VEC>(m, (1u << eb) - 1u);
 }
 
 template <typename TX, int S, bool kEdge, int kFull>
@@ -64,25 +67,31 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
     const Q8& q8 = kMode == kModeQ ? a.q : a.c;
     const bool whole = q8.shift == 31;              // a scale per row
     const int lanes = whole ? W : (1 << q8.shift) / VEC;  // of a group, when rows are whole vectors
-    // kEdge: a vector's elements before eb belong to group ga, the others to the next
-    int ga[KV], eb[KV];
-    bool lead[KV];  // the vector holds its group's first column
+    // Groups of rows that start inside a vector (kEdge): a vector's elements
+    // before eb belong to group ga, the others to the next one.  (W VEC is a
+    // multiple of a group, so eb is the same for all of a thread's vectors;
+    // the row's first vector, which starts before it, has ga = -1.)  Their
+    // maxima meet in shared memory: gm[2][R][ng], used in turn.
+    const bool cutg = kEdge && kMax && !whole;
     constexpr int kIn = kLanes < 32 ? kLanes : 32;
-    const int shift = kEdge && cols.first != 0 ? 1 : 0;
-    float* const gm = reinterpret_cast<float*>(dsm + pl.gm_off);  // [2][R][ng] maxima (kEdge)
-    const bool shared_max = kEdge && kMax && !whole;
-    if constexpr (kMax) {
-#pragma unroll
-        for (int j = 0; j < KV; ++j) {
-            const int c = cols.col(j) < 0 ? 0 : cols.col(j);
-            ga[j] = whole ? 0 : c >> q8.shift;
-            eb[j] = kEdge && !whole ? ((ga[j] + 1) << q8.shift) - cols.col(j) : VEC;
-            lead[j] = cols.ok(j) && (c & (whole ? -1 : (1 << q8.shift) - 1)) == 0;
+    const int shift = kEdge && cols.first != 0 ? 1 : 0;  // lanes by which runs of a group are off
+    int ga0 = 0, eb = VEC;
+    if (kMax && !whole) {
+        ga0 = cols.col(0) >> q8.shift;
+        if (kEdge) {
+            eb = ((ga0 + 1) << q8.shift) - cols.col(0);
+            eb = eb < VEC ? eb : VEC;
         }
-        if (shared_max) {
-            for (int i = threadIdx.x; i < 2 * R * q8.ng; i += W * G) gm[i] = 0.f;
-            __syncthreads();
-        }
+    }
+    const int gstep = whole ? 0 : (W * VEC) >> q8.shift;
+    uint32_t m16[VEC / 2], m8[VEC / 4];
+    before<VEC, VEC / 2>(m16, eb);
+    before<VEC, VEC / 4>(m8, eb);
+    unsigned* const gm = reinterpret_cast<unsigned*>(dsm + pl.gm_off);
+    float* const rsm = reinterpret_cast<float*>(gm + 2 * R * q8.ng);
+    if (cutg) {
+        for (int i = threadIdx.x; i < 2 * R * q8.ng; i += W * G) gm[i] = 0;
+        __syncthreads();
     }
     int half = 0;  // of gm
 
@@ -130,46 +139,59 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
 #pragma unroll
                         for (int p = 0; p < P; ++p) sv[p] = mul2(sv[p], wf[j][p]);
                     }
-                    if (!shared_max) {
+                    auto amax = [&](const f2 (&v)[P]) {
                         float m = 0.f;
-                        if constexpr (kMode == kModeQ) {
 #pragma unroll
-                            for (int p = 0; p < P; ++p)
-                                m = max_nan(max_nan(m, fabsf(lo2(sv[p]))), fabsf(hi2(sv[p])));
-                        } else {
-                            m = vec_amax<TX>(sp[u][j]);
-                        }
+                        for (int p = 0; p < P; ++p)
+                            m = max_nan(max_nan(m, fabsf(lo2(v[p]))), fabsf(hi2(v[p])));
+                        return m;
+                    };
+                    if (!cutg) {
+                        const float m = kMode == kModeQ ? amax(sv) : vec_amax<TX>(sp[u][j]);
                         gmx[u][j] = m;
                         mx[u] = max_nan(mx[u], m);
                     } else {
                         // both groups' shares; the second goes to the next lane,
                         // whose vector starts in that group
-                        float ma = 0.f, mb = 0.f;
+                        const int ga = ga0 + j * gstep;
+                        float ma, mb;
+                        if constexpr (kMode != kModeQ && is16<TX>()) {
+                            const uint4 v = sp[u][j];
+                            ma = vec_amax<TX>(make_uint4(v.x & m16[0], v.y & m16[1], v.z & m16[2],
+                                                         v.w & m16[3]));
+                            mb = vec_amax<TX>(make_uint4(v.x & ~m16[0], v.y & ~m16[1],
+                                                         v.z & ~m16[2], v.w & ~m16[3]));
+                        } else {
+                            f2 va[P], vb[P];
 #pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            const float lo = fabsf(lo2(sv[p])), hi = fabsf(hi2(sv[p]));
-                            if (2 * p < eb[j]) ma = max_nan(ma, lo); else mb = max_nan(mb, lo);
-                            if (2 * p + 1 < eb[j]) ma = max_nan(ma, hi); else mb = max_nan(mb, hi);
+                            for (int p = 0; p < P; ++p) {
+                                const bool b0 = 2 * p < eb, b1 = 2 * p + 1 < eb;
+                                va[p] = mk2(b0 ? lo2(sv[p]) : 0.f, b1 ? hi2(sv[p]) : 0.f);
+                                vb[p] = mk2(b0 ? 0.f : lo2(sv[p]), b1 ? 0.f : hi2(sv[p]));
+                            }
+                            ma = amax(va);
+                            mb = amax(vb);
                         }
-                        const bool two = ok && eb[j] < VEC && ga[j] + 1 < q8.ng;
+                        const bool two = ok && eb < VEC && ga + 1 < q8.ng;
                         const float up = __shfl_up_sync(0xffffffffu, two ? mb : 0.f, 1, kIn);
-                        if ((l & (kIn - 1)) != 0) ma = max_nan(ma, up);
-                        // the lanes of a warp that share a group: aligned runs of
+                        const int lane = l & (kIn - 1);
+                        if (lane != 0) ma = max_nan(ma, up);
+                        // The lanes of a warp that share a group: aligned runs of
                         // `lanes`, one lane further on where rows start inside a
                         // vector (lane 0 then ends a run of the warp before and
                         // stays out).  Magnitudes compare like their bits (NaN on
-                        // top): one atomic a run, whose order does not matter
-                        const bool out = shift && (l & (kIn - 1)) == 0;
+                        // top): one atomic a run, whose order does not matter.
+                        const bool out = shift && lane == 0;
                         float m = out ? 0.f : ma;
                         for (int off = 1; off < lanes; off <<= 1)
                             m = max_nan(m, __shfl_sync(0xffffffffu, m,
-                                                       ((((l - shift) & (kIn - 1)) ^ off) + shift) & (kIn - 1), kIn));
-                        unsigned* const dst = reinterpret_cast<unsigned*>(gm) +
-                                              (half * R + g + u * G) * q8.ng + ga[j];
-                        if (ok && (out || ((l - shift) & (lanes - 1)) == 0))
+                                                       ((((lane - shift) & (kIn - 1)) ^ off) + shift) &
+                                                           (kIn - 1),
+                                                       kIn));
+                        unsigned* const dst = gm + (half * R + g + u * G) * q8.ng + ga;
+                        if (ok && ga >= 0 && (out || ((lane - shift) & (lanes - 1)) == 0))
                             atomicMax(dst, __float_as_uint(out ? ma : m));
-                        if (two && ((l & (kIn - 1)) == kIn - 1 ||
-                                    cols.col(j) + VEC >= N))  // no next lane to take it
+                        if (two && (lane == kIn - 1 || cols.col(j) + VEC >= N))  // no next lane
                             atomicMax(dst + 1, __float_as_uint(mb));
                     }
                 }
@@ -178,25 +200,41 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
         // the row's sum, and its maximum for a scale per row; a group's
         // maximum from its lanes, or from shared memory
         if (kNorm || whole) row_reduce<kLanes, kG, U, kMax>(ss, mx, red, parity, g, l);
-        if constexpr (kMax) {
-            if (shared_max) {
-                __syncthreads();
-            } else if (!whole) {
-                for (int off = 1; off < lanes; off <<= 1)
+        float rs[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) rs[u] = kNorm ? rsqrtf(fmaf(ss[u], a.inv_n, a.eps)) : 1.f;
+        if (cutg) {
+            // a thread per group: its scale, and the factor its elements take
+            if (l == 0) {
 #pragma unroll
-                        for (int j = 0; j < KV; ++j)
-                            gmx[u][j] = max_nan(gmx[u][j],
-                                                __shfl_xor_sync(0xffffffffu, gmx[u][j], off));
+                for (int u = 0; u < U; ++u) rsm[g + u * G] = kMode == kModeQ ? rs[u] : 1.f;
             }
+            __syncthreads();
+            unsigned* const now = gm + half * R * q8.ng;
+            half ^= 1;
+            unsigned* const next = gm + half * R * q8.ng;
+            for (int i = threadIdx.x; i < R * q8.ng; i += W * G) {
+                const int q = i / q8.ng;  // the row
+                const float t = rsm[q], sc = q8_scale(__uint_as_float(now[i]) * t, kType);
+                now[i] = __float_as_uint(t * __frcp_rn(sc));
+                next[i] = 0;
+                if (alive && b * R + q < a.M) q8.scale[b * R * q8.ng + i] = sc;
+            }
+            __syncthreads();
+        } else if (kMax && !whole) {
+            for (int off = 1; off < lanes; off <<= 1)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < KV; ++j)
+                        gmx[u][j] =
+                            max_nan(gmx[u][j], __shfl_xor_sync(0xffffffffu, gmx[u][j], off));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = row + u * G;
-            const float rs = kNorm ? rsqrtf(fmaf(ss[u], a.inv_n, a.eps)) : 1.f;
-            const f2 r2 = splat2(rs);
-            if (kNorm && a.rstd) st_f32_if(l == 0 && okr[u], a.rstd + r, rs);
+            const f2 r2 = splat2(rs[u]);
+            if (kNorm && a.rstd) st_f32_if(l == 0 && okr[u], a.rstd + r, rs[u]);
             const int64_t atu = at + (int64_t)u * G * N;
 #pragma unroll
             for (int j = 0; j < KV; ++j) {
@@ -218,44 +256,41 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
                                cols.cut(j), cols.em[j]);
                 }
                 if constexpr (kMax) {
-                    float ma = whole ? mx[u] : gmx[u][j], mb = 0.f;
-                    if (shared_max && ok) {
-                        const float* m = gm + (half * R + g + u * G) * q8.ng + ga[j];
-                        ma = m[0];
-                        mb = eb[j] < VEC && ga[j] + 1 < q8.ng ? m[1] : 0.f;
-                    }
                     if constexpr (kMode == kModeQ) {
 #pragma unroll
                         for (int p = 0; p < P; ++p) sv[p] = mul2(sv[p], wf[j][p]);
                     }
-                    const float t = kMode == kModeQ ? rs : 1.f;  // r enters here
-                    const float sa = q8_scale(ma * t, kType);
-                    const float ka = t * __frcp_rn(sa);
-                    float sb = 0.f, kb = ka;
-                    if (shared_max) {
-                        sb = q8_scale(mb * t, kType);
-                        kb = t * __frcp_rn(sb);
-                    }
                     uint32_t o[VEC / 4];
-                    pack_vec8<VEC, kEdge, kType>(o, sv, ka, kb, eb[j]);
+                    const int ga = ga0 + j * gstep;
+                    if (cutg) {
+                        // the other half of gm: `half` was turned
+                        const unsigned* k = gm + ((half ^ 1) * R + g + u * G) * q8.ng + ga;
+                        const bool two = ok && eb < VEC && ga + 1 < q8.ng;
+                        const float ka = ok && ga >= 0 ? __uint_as_float(k[0]) : 0.f;
+                        const float kb = two ? __uint_as_float(k[1]) : 0.f;
+                        uint32_t ob[VEC / 4];
+                        pack_vec8<VEC, kType>(o, sv, ka);
+                        pack_vec8<VEC, kType>(ob, sv, kb);
+#pragma unroll
+                        for (int i = 0; i < VEC / 4; ++i) o[i] = (o[i] & m8[i]) | (ob[i] & ~m8[i]);
+                    } else {
+                        const float t = kMode == kModeQ ? rs[u] : 1.f;  // r enters here
+                        const float sc = q8_scale((whole ? mx[u] : gmx[u][j]) * t, kType);
+                        pack_vec8<VEC, kType>(o, sv, t * __frcp_rn(sc));
+                        // the vector that holds a group's first column writes its scale
+                        const int c = cols.col(j) < 0 ? 0 : cols.col(j);
+                        if (ok && (c & (whole ? -1 : (1 << q8.shift) - 1)) == 0)
+                            q8.scale[r * q8.ng + ga] = sc;
+                    }
                     st_vec8<VEC>(static_cast<unsigned char*>(q8.v) + atu + j * W * VEC, o, ok,
                                  cols.cut(j), cols.em[j]);
-                    // the vector that holds a group's first column writes its scale
-                    float* const sc = q8.scale + r * q8.ng + ga[j];
-                    if (okr[u] && lead[j]) sc[0] = sa;
-                    if (shared_max && ok && eb[j] < VEC && ga[j] + 1 < q8.ng) sc[1] = sb;
                 }
             }
         }
         row += row_step;
         at += at_step;
-        if (shared_max) {
-            // the other half is free: its readers passed the barrier above
-            half ^= 1;
-            for (int i = threadIdx.x; i < R * q8.ng; i += W * G) gm[half * R * q8.ng + i] = 0.f;
-            return false;  // and a barrier before its next use
-        }
-        return kLanes > 32 && (kNorm || whole);  // row_reduce's barrier came after the last slot read
+        // a barrier came after the last read of the slot
+        return cutg || (kLanes > 32 && (kNorm || whole));
     });
 }
 

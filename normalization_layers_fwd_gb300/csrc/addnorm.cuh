@@ -75,8 +75,8 @@ struct UnpackArgs {
 struct RowPlan {
     int sid, edge, grid;
     int W, G;              // threads of a row group, row groups of a CTA
-    int plain;             // every input's rows in order, of whole 16-byte units
-    uint32_t block_bytes;  // of a whole block, all inputs
+    int in_order;          // every input's rows are in order
+    int tail;              // some input does not end on a 16-byte boundary
     int64_t nblocks;
     int R, stages;
     uint32_t off[3], stage_bytes, gm_off;  // gm_off: the group maxima's place
@@ -94,6 +94,9 @@ cudaError_t launch_add_fwd_f32(cudaStream_t st, int mode, const FwdArgs& a, cons
 cudaError_t launch_add_bwd_bf16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_bwd_f16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_bwd_f32(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
+// act_pack8 and act_unpack8 over the storage, vector by vector (pack8.cu):
+// contiguous tensors on 16-byte boundaries; to pack, rows of whole groups.
+cudaError_t launch_pack_fast(cudaStream_t st, int xt, int sms, const FwdArgs& a);
 cudaError_t launch_unpack_fast(cudaStream_t st, int xt, int sms, const UnpackArgs& a);
 
 // Launches of the general kernels (any width, alignment and layout).

@@ -1,6 +1,9 @@
-// unpack8.cu -- 8-bit values back to activations.
+// pack8.cu -- activations to 8-bit values and back, over the storage.
 //
-// Elementwise over the storage: a thread takes vectors of VEC consecutive
+// Packing rows of whole groups: a group is `lanes` vectors in a row, of
+// adjacent lanes, wherever its row begins; its maximum is a butterfly over
+// them.  No shared memory and no barrier: kBatch vectors a thread in flight.
+// Unpacking, elementwise: a thread takes vectors of VEC consecutive
 // elements of [M, N], kBatch at once with all of their loads in flight, and
 // follows their row and column without a division (each step adds a fixed
 // number of rows and columns).  A vector inside one group needs one scale; at
@@ -89,6 +92,61 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+template <typename TX, int kType>
+__global__ void __launch_bounds__(kThreads) pack_vec(const __grid_constant__ FwdArgs a)
+{
+    grid_dependency_sync();
+    constexpr int VEC = Vec<TX>::kN, P = VEC / 2;
+    const int lanes = (1 << a.c.shift) / VEC;  // of a group: divides 32
+    const int64_t total = a.M * a.N / VEC, step = (int64_t)gridDim.x * kThreads;
+    const uint4* x = reinterpret_cast<const uint4*>(a.in[0].p);
+    unsigned char* q = static_cast<unsigned char*>(a.c.v);
+    const int64_t v0 = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    // the same trip count for a whole warp: the butterflies need all lanes
+    for (int64_t w = v0 - (threadIdx.x & 31); w < total; w += kBatch * step) {
+        const int64_t v = w + (threadIdx.x & 31);
+        uint4 u[kBatch];
+        float m[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            u[i] = v + i * step < total ? __ldcs(x + v + i * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) m[i] = vec_amax<TX>(u[i]);
+        for (int off = 1; off < lanes; off <<= 1)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t at = v + i * step;
+            if (at >= total) break;
+            const float sc = q8_scale(m[i], kType);
+            const f2 k = splat2(__frcp_rn(sc));
+            f2 f[P];
+            unpack2<TX>(u[i], f);
+            if constexpr (VEC == 8)
+                __stcs(reinterpret_cast<uint2*>(q) + at,
+                       make_uint2(q8_pack4<kType>(f[0], f[1], k, k),
+                                  q8_pack4<kType>(f[2], f[3], k, k)));
+            else
+                __stcs(reinterpret_cast<unsigned*>(q) + at, q8_pack4<kType>(f[0], f[1], k, k));
+            if ((threadIdx.x & (lanes - 1)) == 0) a.c.scale[at / lanes] = sc;
+        }
+    }
+}
+
+template <typename TX>
+void pack_launch(cudaStream_t st, int sms, const FwdArgs& a)
+{
+    const int64_t total = a.M * a.N / Vec<TX>::kN, per = (int64_t)kThreads * kBatch;
+    const int64_t ctas = (total + per - 1) / per, cap = 8LL * sms;
+    const unsigned grid = (unsigned)(ctas < cap ? ctas : cap);
+    if (a.c.type == kE4M3)
+        launch_pdl(pack_vec<TX, kE4M3>, grid, kThreads, 0, st, a);
+    else
+        launch_pdl(pack_vec<TX, kInt8>, grid, kThreads, 0, st, a);
+}
+
 template <typename TX>
 void unpack_launch(cudaStream_t st, int sms, const UnpackArgs& a)
 {
@@ -107,6 +165,17 @@ void unpack_launch(cudaStream_t st, int sms, const UnpackArgs& a)
 }
 
 }  // namespace
+
+cudaError_t launch_pack_fast(cudaStream_t st, int xt, int sms, const FwdArgs& a)
+{
+    if (xt == kF32)
+        pack_launch<float>(st, sms, a);
+    else if (xt == kF16)
+        pack_launch<__half>(st, sms, a);
+    else
+        pack_launch<__nv_bfloat16>(st, sms, a);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_unpack_fast(cudaStream_t st, int xt, int sms, const UnpackArgs& a)
 {

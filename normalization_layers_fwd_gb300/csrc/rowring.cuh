@@ -81,7 +81,7 @@ constexpr int row_minb(int kind, int S, bool edge)
     const RowSched& e = row_sched(kind, S);
     return e.T == 512    ? 1
            : kind == kKindB ? 2
-           : e.KV == 1      ? (edge ? 3 : 4)
+           : e.KV == 1      ? 3
            : e.KV == 2 && kind != kKindF ? 3
                                          : 2;
 }
@@ -96,22 +96,10 @@ constexpr int kMaxSmem = 208 * 1024;
 #ifdef __CUDACC__
 
 // ------------------------------------------------------------------ ring
-// Byte range of block b of a contiguous input that a bulk copy moves, and the
-// end of its rows.
-struct Span {
-    int64_t start, end, rows_end;
-};
-__device__ __forceinline__ Span row_span(const RowSrc& s, int64_t r0, int rows)
-{
-    Span p;
-    p.start = (r0 * s.row_bytes) & ~(int64_t)15;
-    p.rows_end = (r0 + rows) * s.row_bytes;
-    const int64_t whole = s.total & ~(int64_t)15, up = (p.rows_end + 15) & ~(int64_t)15;
-    p.end = up < whole ? up : whole;
-    return p;
-}
-
-// Block b into stage st: every lane of warp 0.
+// Block b into stage st: every lane of warp 0.  Lane t takes input t (the
+// barrier counts an arrival per input), so a block costs one input's
+// arithmetic: the other warps meet this one at every row's barrier, and
+// taking the inputs one after another on one lane cost the backwards 5-25%.
 template <int NT>
 __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan& pl, int64_t M,
                                           unsigned char* dsm, int64_t b, int st)
@@ -120,49 +108,42 @@ __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan&
     unsigned char* const slot = dsm + 128 + (size_t)st * pl.stage_bytes;
     const int lane = threadIdx.x & 31;
     const int64_t r0 = b * pl.R;
-    if (pl.plain && b < pl.nblocks - 1) {
-        // a whole block of rows in order, each of whole 16-byte units: the
-        // usual case, one lane with a product and a copy per input
-        if (lane == 0) {
-            mbar_expect_tx(bar, pl.block_bytes);
+    // lane t's input (selects: indexing the parameters would copy them)
+    const unsigned char* p = nullptr;
+    uint32_t rb = 0, off = 0;
+    int64_t total = 0;
+    int scattered = 0;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (in[t].p) {
-                    const uint32_t n = (uint32_t)pl.R * (uint32_t)in[t].row_bytes;
-                    bulk_g2s(slot + pl.off[t], in[t].p + b * (int64_t)n, n, bar);
-                }
+    for (int t = 0; t < NT; ++t)
+        if (lane == t) {
+            p = in[t].p;
+            rb = (uint32_t)in[t].row_bytes;
+            total = in[t].total;
+            scattered = in[t].scattered;
+            off = pl.off[t];
         }
-        return;
-    }
-    const int rows = (int)(M - r0 < pl.R ? M - r0 : pl.R);
-    int64_t start[NT];
-    uint32_t n[NT], sum = 0;
-    bool scattered = false;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        n[t] = 0;
-        if (!in[t].p) continue;
-        if (in[t].scattered) {
-            scattered = true;
-            n[t] = (uint32_t)(rows * in[t].row_bytes);
+    if (p) {
+        const bool last = b == pl.nblocks - 1;
+        if (scattered) {
+            mbar_expect_tx(bar, (uint32_t)(last ? (int)(M - r0) : pl.R) * rb);
         } else {
-            const Span sp = row_span(in[t], r0, rows);
-            start[t] = sp.start;
-            n[t] = sp.end > sp.start ? (uint32_t)(sp.end - sp.start) : 0;
+            // from the 16-byte boundary below the block to the one above it;
+            // the last block's end is clipped to the input's whole units
+            const uint32_t rows = (uint32_t)pl.R * rb;
+            const int64_t at = b * (int64_t)rows;
+            const uint32_t low = (uint32_t)at & 15u;
+            uint32_t n = (low + rows + 15u) & ~15u;
+            if (last) n = (uint32_t)((total & ~(int64_t)15) - (at - low));
+            mbar_expect_tx(bar, n);
+            if (n) bulk_g2s(slot + off, p + (at - low), n, bar);
         }
-        sum += n[t];
     }
-    if (lane == 0) {
-        mbar_expect_tx(bar, sum);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (n[t] && !in[t].scattered) bulk_g2s(slot + pl.off[t], in[t].p + start[t], n[t], bar);
-    }
-    if (scattered) {
+    if (!pl.in_order) {
+        const int rows = (int)(M - r0 < pl.R ? M - r0 : pl.R);
         __syncwarp();  // the expected bytes are set before a copy lands
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            if (n[t] && in[t].scattered)
+            if (in[t].p && in[t].scattered)
                 for (int i = lane; i < rows; i += 32)
                     bulk_g2s(slot + pl.off[t] + i * (uint32_t)in[t].row_bytes,
                              in[t].p + row_byte_offset(in[t].map, r0 + i),
@@ -173,19 +154,15 @@ __device__ __forceinline__ void row_issue(const RowSrc (&in)[NT], const RowPlan&
 // The bytes of block b past the inputs' whole 16-byte units, into the slot:
 // every thread, once the block's copies have landed; the caller synchronizes.
 template <int NT>
-__device__ __noinline__ void row_tail(const RowSrc (&in)[NT], const RowPlan& pl, int64_t M,
+__device__ __noinline__ void row_tail(const RowSrc (&in)[NT], const RowPlan& pl,
                                       unsigned char* slot, int64_t b)
 {
-    const int64_t r0 = b * pl.R;
-    const int rows = (int)(M - r0 < pl.R ? M - r0 : pl.R);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (!in[t].p || in[t].scattered) continue;
-        const Span sp = row_span(in[t], r0, rows);
-        const int64_t from = sp.end > sp.start ? sp.end : sp.start;
-        if (from >= sp.rows_end) continue;
-        const int i = threadIdx.x;
-        if (from + i < sp.rows_end) slot[pl.off[t] + (from - sp.start) + i] = in[t].p[from + i];
+        const int64_t start = (b * pl.R * in[t].row_bytes) & ~(int64_t)15;
+        const int64_t i = (in[t].total & ~(int64_t)15) + threadIdx.x;
+        if (i < in[t].total) slot[pl.off[t] + (i - start)] = in[t].p[i];
     }
 }
 
@@ -198,7 +175,10 @@ __device__ __forceinline__ int64_t row_ring_start(const RowSrc (&in)[NT], const 
                           ? (pl.nblocks - 1 - blockIdx.x) / gridDim.x + 1
                           : 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < pl.stages; ++s) mbar_init(reinterpret_cast<uint64_t*>(dsm) + s, 1);
+        int n = 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) n += in[t].p != nullptr;
+        for (int s = 0; s < pl.stages; ++s) mbar_init(reinterpret_cast<uint64_t*>(dsm) + s, n);
         fence_mbar_init();
     }
     __syncthreads();
@@ -228,8 +208,8 @@ __device__ __forceinline__ void row_ring(const RowSrc (&in)[NT], const RowPlan& 
             alive = mbar_wait(&bar[st], phase, pl.fault);
             if (!alive) failed_at = k;
         }
-        if (!pl.plain && b == pl.nblocks - 1) {  // uniform; a failed wait loads nothing below
-            row_tail(in, pl, M, slot, b);
+        if (pl.tail && b == pl.nblocks - 1) {  // uniform; a failed wait loads nothing below
+            row_tail(in, pl, slot, b);
             __syncthreads();
         }
         if (!body(b, slot, alive)) __syncthreads();

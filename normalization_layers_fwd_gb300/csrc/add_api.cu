@@ -204,9 +204,7 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     const int mode =
         (!f.w ? gbn::kModeC : f.q.v ? gbn::kModeQ : f.c.v ? gbn::kModeYC : gbn::kModeY) +
         (q8.v && q8.type == gbn::kInt8 ? gbn::kModeInt8 : 0);
-    // a checkpoint alone, of rows of whole groups, needs no row at all
-    if (!f.w && q8.shift != 31 && N % (1 << q8.shift) == 0 && !a.in[0].scattered &&
-        aligned(16, {f.x, q8.v}))
+    if (!f.w && gbn::pack_fast(f.xt, a))  // a checkpoint alone, of rows of whole groups
         return launch_status(gbn::launch_pack_fast(stream, f.xt, sms, a));
     gbn::RowPlan p;
     if (!plan_rows(p, gbn::fwd_kind(mode), f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))

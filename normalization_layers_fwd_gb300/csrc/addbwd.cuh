@@ -47,15 +47,20 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
     const uint32_t so1 = pl.off[1] + row_off(a.in[1], row - g, g) - cols.first * E + l * 16;
     const uint32_t so2 = pl.off[2] + row_off(a.in[2], row - g, g) - cols.first * E + l * 16;
 
-    // A row's rstd, and the scales of its vectors' groups, are loaded one row
-    // block ahead of their use.  kEdge: elements from eb on take the second.
+    // A row's rstd, and the scale of each vector's group, are loaded one row
+    // block ahead of their use.  kEdge: a vector's elements before eb belong to
+    // group ga, the others to the next one, whose scale the next lane holds
+    // (vectors that span two groups are never a warp's last: groups are aligned
+    // runs of lanes, one lane further on; the row's first vector, which starts
+    // before it, has ga = -1).
     const bool whole = !kPacked || a.c.shift == 31;
-    auto group_of = [&](int j) {
-        const int c = cols.col(j) < 0 ? 0 : cols.col(j);
-        return whole ? 0 : c >> a.c.shift;
-    };
-    constexpr int kSc = kPacked ? (kEdge ? 2 : 1) : 0;
-    float rs_n[U], sc_n[U][KV][kSc ? kSc : 1];
+    int ga0 = 0, eb = VEC;
+    if (kPacked && !whole) {
+        ga0 = cols.col(0) >> a.c.shift;
+        if (kEdge) eb = ((ga0 + 1) << a.c.shift) - cols.col(0);
+    }
+    const int gstep = whole ? 0 : (W * VEC) >> a.c.shift;
+    float rs_n[U], sc_n[U][kPacked ? KV : 1];
     auto load_stats = [&](int64_t row0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -66,10 +71,8 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
                 const float* const scr = a.c.scale + r * a.c.ng;
 #pragma unroll
                 for (int j = 0; j < KV; ++j) {
-                    const int q = group_of(j);
-                    sc_n[u][j][0] = in && cols.ok(j) ? __ldca(scr + q) : 0.f;
-                    if constexpr (kEdge)
-                        sc_n[u][j][1] = in && cols.ok(j) && q + 1 < a.c.ng ? __ldca(scr + q + 1) : 0.f;
+                    const int q = ga0 + j * gstep;
+                    sc_n[u][j] = in && q >= 0 && q < a.c.ng ? __ldca(scr + q) : 0.f;
                 }
             }
         }
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
 
     row_ring(a.in, pl, a.M, dsm, K, [&](int64_t b, const unsigned char* slot, bool alive) {
         const bool last = b == pl.nblocks - 1;
-        float rs[U], sc[U][KV][kSc ? kSc : 1], sum[U], none[U];
+        float rs[U], sc[U][kPacked ? KV : 1], sum[U], none[U];
         bool okr[U];
         // a block of 8-bit rows may start anywhere in a 16-byte unit
         const uint32_t sc0 = kPacked ? ((uint32_t)(b * R) * (uint32_t)N) & 15u : 0u;
@@ -88,9 +91,7 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
             rs[u] = rs_n[u];
             if constexpr (kPacked) {
 #pragma unroll
-                for (int j = 0; j < KV; ++j)
-#pragma unroll
-                    for (int q = 0; q < kSc; ++q) sc[u][j][q] = sc_n[u][j][q] * rs[u];
+                for (int j = 0; j < KV; ++j) sc[u][j] = sc_n[u][j] * rs[u];
             }
         }
         auto ld_s = [&](int u, int j, uint32_t (&v)[NS]) {
@@ -131,14 +132,13 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
                 for (int i = 0; i < VEC / 4; ++i)
                     q8_unpack4<kType>(sp[u][j][i], xh[2 * i], xh[2 * i + 1]);
                 if constexpr (kEdge) {
-                    const int eb = whole ? VEC : ((group_of(j) + 1) << a.c.shift) - cols.col(j);
-                    const float ka = sc[u][j][0], kb = sc[u][j][kSc - 1];
+                    const float ka = sc[u][j], kb = __shfl_down_sync(0xffffffffu, ka, 1);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
                         xh[p] = mul2(xh[p], mk2(2 * p < eb ? ka : kb, 2 * p + 1 < eb ? ka : kb));
                 } else {
 #pragma unroll
-                    for (int p = 0; p < P; ++p) xh[p] = mul2(xh[p], splat2(sc[u][j][0]));
+                    for (int p = 0; p < P; ++p) xh[p] = mul2(xh[p], splat2(sc[u][j]));
                 }
             } else {
                 unpack2<TX>(make_uint4(sp[u][j][0], sp[u][j][1], sp[u][j][2], sp[u][j][3]), xh);
@@ -213,7 +213,17 @@ __global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
     // `first` of that group's rows further on.
     const int cap = W * KV * VEC;
     float* const out = a.ws + blockIdx.x * (int64_t)N;
-    if (G == 1) {
+    if (G == 1 && !kEdge && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < KV; ++j)
+            if (cols.ok(j)) {
+#pragma unroll
+                for (int p = 0; p < P; p += 2)
+                    *reinterpret_cast<float4*>(out + cols.col(j) + 2 * p) =
+                        make_float4(lo2(acc[j][p]), hi2(acc[j][p]), lo2(acc[j][p + 1]),
+                                    hi2(acc[j][p + 1]));
+            }
+    } else if (G == 1) {
 #pragma unroll
         for (int j = 0; j < KV; ++j)
 #pragma unroll

@@ -94,8 +94,10 @@ cudaError_t launch_add_fwd_f32(cudaStream_t st, int mode, const FwdArgs& a, cons
 cudaError_t launch_add_bwd_bf16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_bwd_f16(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_bwd_f32(cudaStream_t st, int mode, const BwdArgs& a, const RowPlan& p);
-// act_pack8 and act_unpack8 over the storage, vector by vector (pack8.cu):
-// contiguous tensors on 16-byte boundaries; to pack, rows of whole groups.
+// act_pack8 and act_unpack8 over the storage (pack8.cu), for contiguous
+// tensors: to pack where pack_fast says so (rows of whole groups), to unpack
+// on 16-byte boundaries.
+bool pack_fast(int xt, const FwdArgs& a);
 cudaError_t launch_pack_fast(cudaStream_t st, int xt, int sms, const FwdArgs& a);
 cudaError_t launch_unpack_fast(cudaStream_t st, int xt, int sms, const UnpackArgs& a);
 

@@ -1,9 +1,10 @@
 // pack8.cu -- activations to 8-bit values and back, over the storage.
 //
-// Packing rows of whole groups: a group is `lanes` vectors in a row, of
-// adjacent lanes, wherever its row begins; its maximum is a butterfly over
-// them.  No shared memory and no barrier: kBatch vectors a thread in flight.
-// Unpacking, elementwise: a thread takes vectors of VEC consecutive
+// Units of 32 bytes of x (16 16-bit elements, 8 float32): one load, one store
+// and one scale each.  Packing rows of whole groups, a group is a run of
+// adjacent lanes wherever its row begins, and its maximum a butterfly over
+// them: no shared memory, no barrier, kBatch units a thread in flight.
+// Unpacking rows that are not whole units, by vectors: a thread takes vectors of VEC consecutive
 // elements of [M, N], kBatch at once with all of their loads in flight, and
 // follows their row and column without a division (each step adds a fixed
 // number of rows and columns).  A vector inside one group needs one scale; at
@@ -92,79 +93,191 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// 32 bytes of activations, one load or store each.
+struct Unit32 {
+    uint4 a, b;
+};
+__device__ __forceinline__ Unit32 ld_unit(const void* p)
+{
+    Unit32 u;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u.a.x), "=r"(u.a.y), "=r"(u.a.z), "=r"(u.a.w), "=r"(u.b.x), "=r"(u.b.y),
+                   "=r"(u.b.z), "=r"(u.b.w)
+                 : "l"(p));
+    return u;
+}
+__device__ __forceinline__ void st_unit(void* p, const Unit32& u)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u.a.x),
+                 "r"(u.a.y), "r"(u.a.z), "r"(u.a.w), "r"(u.b.x), "r"(u.b.y), "r"(u.b.z),
+                 "r"(u.b.w)
+                 : "memory");
+}
+
+// A lane takes units of 32 bytes of x.  lanes: units of a group (or of a row
+// with one scale), a power of two of at most 32.
 template <typename TX, int kType>
-__global__ void __launch_bounds__(kThreads) pack_vec(const __grid_constant__ FwdArgs a)
+__global__ void __launch_bounds__(kThreads)
+    pack_units(const __grid_constant__ FwdArgs a, int lanes, int log_lanes)
 {
     grid_dependency_sync();
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2;
-    const int lanes = (1 << a.c.shift) / VEC;  // of a group: divides 32
-    const int64_t total = a.M * a.N / VEC, step = (int64_t)gridDim.x * kThreads;
-    const uint4* x = reinterpret_cast<const uint4*>(a.in[0].p);
+    const int64_t total = a.M * a.N / (2 * VEC), step = (int64_t)gridDim.x * kThreads;
+    const unsigned char* x = a.in[0].p;
     unsigned char* q = static_cast<unsigned char*>(a.c.v);
-    const int64_t v0 = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    const int lane = threadIdx.x & 31;
     // the same trip count for a whole warp: the butterflies need all lanes
-    for (int64_t w = v0 - (threadIdx.x & 31); w < total; w += kBatch * step) {
-        const int64_t v = w + (threadIdx.x & 31);
-        uint4 u[kBatch];
+    for (int64_t w = blockIdx.x * (int64_t)kThreads + threadIdx.x - lane; w < total;
+         w += kBatch * step) {
+        Unit32 u[kBatch];
         float m[kBatch];
+        bool ok[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            u[i] = v + i * step < total ? __ldcs(x + v + i * step) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t v = w + i * step + lane;
+            ok[i] = v < total;
+            if (ok[i])
+                u[i] = ld_unit(x + v * 32);
+            else
+                u[i].a = u[i].b = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) m[i] = vec_amax<TX>(u[i]);
+        for (int i = 0; i < kBatch; ++i) m[i] = max_nan(vec_amax<TX>(u[i].a), vec_amax<TX>(u[i].b));
         for (int off = 1; off < lanes; off <<= 1)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int64_t at = v + i * step;
-            if (at >= total) break;
+            const int64_t v = w + i * step + lane;
             const float sc = q8_scale(m[i], kType);
             const f2 k = splat2(__frcp_rn(sc));
-            f2 f[P];
-            unpack2<TX>(u[i], f);
+            f2 f[P], g[P];
+            unpack2<TX>(u[i].a, f);
+            unpack2<TX>(u[i].b, g);
+            if (!ok[i]) continue;
             if constexpr (VEC == 8)
-                __stcs(reinterpret_cast<uint2*>(q) + at,
-                       make_uint2(q8_pack4<kType>(f[0], f[1], k, k),
-                                  q8_pack4<kType>(f[2], f[3], k, k)));
+                __stcs(reinterpret_cast<uint4*>(q) + v,
+                       make_uint4(q8_pack4<kType>(f[0], f[1], k, k), q8_pack4<kType>(f[2], f[3], k, k),
+                                  q8_pack4<kType>(g[0], g[1], k, k),
+                                  q8_pack4<kType>(g[2], g[3], k, k)));
             else
-                __stcs(reinterpret_cast<unsigned*>(q) + at, q8_pack4<kType>(f[0], f[1], k, k));
-            if ((threadIdx.x & (lanes - 1)) == 0) a.c.scale[at / lanes] = sc;
+                __stcs(reinterpret_cast<uint2*>(q) + v,
+                       make_uint2(q8_pack4<kType>(f[0], f[1], k, k),
+                                  q8_pack4<kType>(g[0], g[1], k, k)));
+            if ((lane & (lanes - 1)) == 0) a.c.scale[v >> log_lanes] = sc;
         }
     }
+}
+
+// Units of 32 bytes of x that lie in one row and one group each.
+template <typename TX, int kType>
+__global__ void __launch_bounds__(kThreads)
+    unpack_units(const __grid_constant__ UnpackArgs a, int64_t step_rows, int step_cols)
+{
+    grid_dependency_sync();
+    constexpr int VEC = Vec<TX>::kN, P = VEC / 2;
+    const int64_t total = a.M * a.N / (2 * VEC), step = (int64_t)gridDim.x * kThreads;
+    const unsigned char* q = static_cast<const unsigned char*>(a.c.v);
+    unsigned char* x = static_cast<unsigned char*>(a.x);
+    int64_t v = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    int64_t r = v * (2 * VEC) / a.N;
+    int c = (int)(v * (2 * VEC) - r * a.N);
+    for (; v < total; v += kBatch * step) {
+        uint32_t w[kBatch][VEC / 2];
+        float s[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (v + i * step < total) {
+                if constexpr (VEC == 8) {
+                    const uint4 t = __ldcs(reinterpret_cast<const uint4*>(q) + v + i * step);
+                    w[i][0] = t.x, w[i][1] = t.y, w[i][2] = t.z, w[i][3] = t.w;
+                } else {
+                    const uint2 t = __ldcs(reinterpret_cast<const uint2*>(q) + v + i * step);
+                    w[i][0] = t.x, w[i][1] = t.y;
+                }
+                s[i] = __ldg(a.c.scale + r * a.c.ng + (c >> a.c.shift));
+            }
+            r += step_rows;
+            c += step_cols;
+            if (c >= a.N) {
+                c -= a.N;
+                ++r;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (v + i * step >= total) break;
+            f2 f[P], g[P];
+#pragma unroll
+            for (int h = 0; h < VEC / 4; ++h) {
+                q8_unpack4<kType>(w[i][h], f[2 * h], f[2 * h + 1]);
+                q8_unpack4<kType>(w[i][VEC / 4 + h], g[2 * h], g[2 * h + 1]);
+            }
+            const f2 k = splat2(s[i]);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                f[p] = mul2(f[p], k);
+                g[p] = mul2(g[p], k);
+            }
+            st_unit(x + (v + i * step) * 32, Unit32{pack2<TX>(f), pack2<TX>(g)});
+        }
+    }
+}
+
+bool on_boundary(const void* p, int bytes)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
+}
+
+unsigned persistent(int64_t units, int per_sm, int sms)
+{
+    const int64_t ctas = (units + kThreads * kBatch - 1) / (kThreads * kBatch);
+    const int64_t cap = (int64_t)per_sm * sms;
+    return (unsigned)(ctas < 1 ? 1 : ctas < cap ? ctas : cap);
 }
 
 template <typename TX>
 void pack_launch(cudaStream_t st, int sms, const FwdArgs& a)
 {
-    const int64_t total = a.M * a.N / Vec<TX>::kN, per = (int64_t)kThreads * kBatch;
-    const int64_t ctas = (total + per - 1) / per, cap = 8LL * sms;
-    const unsigned grid = (unsigned)(ctas < cap ? ctas : cap);
+    constexpr int kUnit = 2 * Vec<TX>::kN;
+    const unsigned grid = persistent(a.M * a.N / kUnit, 8, sms);
+    const int lanes = (a.c.shift == 31 ? a.N : 1 << a.c.shift) / kUnit;
+    int log_lanes = 0;
+    while ((1 << log_lanes) < lanes) ++log_lanes;
     if (a.c.type == kE4M3)
-        launch_pdl(pack_vec<TX, kE4M3>, grid, kThreads, 0, st, a);
+        launch_pdl(pack_units<TX, kE4M3>, grid, kThreads, 0, st, a, lanes, log_lanes);
     else
-        launch_pdl(pack_vec<TX, kInt8>, grid, kThreads, 0, st, a);
+        launch_pdl(pack_units<TX, kInt8>, grid, kThreads, 0, st, a, lanes, log_lanes);
 }
 
 template <typename TX>
 void unpack_launch(cudaStream_t st, int sms, const UnpackArgs& a)
 {
     constexpr int VEC = Vec<TX>::kN;
-    const int64_t whole = a.M * a.N / VEC, per = (int64_t)kThreads * kBatch;
-    const int64_t ctas = (whole + per - 1) / per, cap = 8LL * sms;
-    const int64_t grid = ctas < 1 ? 1 : ctas < cap ? ctas : cap;
-    const int64_t step = grid * kThreads * VEC;
-    auto go = [&](auto kernel) {
-        launch_pdl(kernel, (unsigned)grid, kThreads, 0, st, a, step / a.N, (int)(step % a.N));
+    auto go = [&](auto kernel, int per) {  // `per` elements a thread and turn
+        const unsigned grid = persistent(a.M * a.N / per, 8, sms);
+        const int64_t step = (int64_t)grid * kThreads * per;
+        launch_pdl(kernel, grid, kThreads, 0, st, a, step / a.N, (int)(step % a.N));
     };
+    // a unit's columns start at a multiple of its size, and so do groups
+    const bool units = a.N % (2 * VEC) == 0 && on_boundary(a.x, 32);
     if (a.c.type == kE4M3)
-        go(unpack_vec<TX, kE4M3>);
+        units ? go(unpack_units<TX, kE4M3>, 2 * VEC) : go(unpack_vec<TX, kE4M3>, VEC);
     else
-        go(unpack_vec<TX, kInt8>);
+        units ? go(unpack_units<TX, kInt8>, 2 * VEC) : go(unpack_vec<TX, kInt8>, VEC);
 }
 
 }  // namespace
+
+bool pack_fast(int xt, const FwdArgs& a)
+{
+    const int unit = xt == kF32 ? 8 : 16, N = a.N;
+    if (a.in[0].scattered || !on_boundary(a.in[0].p, 32) || !on_boundary(a.c.v, 16)) return false;
+    if (a.c.shift != 31) return N % (1 << a.c.shift) == 0;
+    const int lanes = N / unit;  // one scale a row
+    return N % unit == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0;
+}
 
 cudaError_t launch_pack_fast(cudaStream_t st, int xt, int sms, const FwdArgs& a)
 {

@@ -95,14 +95,14 @@ struct RowShape {
     int W, G, R;
     int64_t ctas;
 };
-RowShape row_shape(int kind, int sid, int64_t nvec, bool edge, int sms)
+RowShape row_shape(int kind, int sid, int64_t nvec, int sms)
 {
     const gbn::RowSched& e = gbn::row_sched(kind, sid);
     RowShape s;
     s.W = e.W ? e.W : (int)((nvec + 32 * e.KV - 1) / (32 * e.KV)) * 32;
     s.G = gbn::row_G(kind, sid, s.W);
     s.R = s.G * gbn::row_U(kind, sid);
-    const int minb = gbn::row_minb(kind, sid, edge);
+    const int minb = gbn::row_minb(kind, sid);
     // a CTA below its launch bound's size: as many as the same registers hold
     s.ctas = (int64_t)sms * (minb * e.T / (s.W * s.G));
     // rows that start inside a vector need CTAs to step by a multiple of VEC rows
@@ -130,7 +130,7 @@ bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const Ro
     const int64_t nvec = row_vectors(N, vec, p.edge);
     p.sid = find_sched(kind, in[0].row_bytes == N && kind == gbn::kKindB, nvec);
     if (p.sid < 0) return false;
-    const RowShape sh = row_shape(kind, p.sid, nvec, p.edge, sms);
+    const RowShape sh = row_shape(kind, p.sid, nvec, sms);
     p.W = sh.W;
     p.G = sh.G;
     p.R = sh.R;
@@ -288,7 +288,7 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
     for (const bool packed : {false, true}) {
         const int sid = find_sched(kKindB, packed, nvec);
         if (sid < 0) continue;
-        const RowShape sh = row_shape(kKindB, sid, nvec, edge, sms);
+        const RowShape sh = row_shape(kKindB, sid, nvec, sms);
         const int64_t blocks = (M + sh.R - 1) / sh.R, grid = blocks < sh.ctas ? blocks : sh.ctas;
         P = P > grid ? P : grid;
     }

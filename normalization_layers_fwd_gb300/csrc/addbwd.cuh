@@ -9,11 +9,11 @@ namespace gbn {
 namespace {
 
 template <typename TX, int S, bool kEdge, int kMode>
-__global__ void __launch_bounds__(kRowB[S].T, row_minb(kKindB, S, kEdge))
+__global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
     add_bwd_ring(const __grid_constant__ BwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();
-    constexpr int kW = kRowB[S].W, KV = kRowB[S].KV, U = row_U(kKindB, S);
+    constexpr int kW = kRow2[S].W, KV = kRow2[S].KV, U = row_U(kKindB, S);
     constexpr int kG = row_G(kKindB, S), kLanes = kW ? kW : 256;
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
     constexpr bool kPacked = kMode >= kBwdC, kCast = kMode == kBwdCast, kLean = KV > 2;

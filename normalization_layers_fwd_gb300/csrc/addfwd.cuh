@@ -31,7 +31,7 @@ __device__ __forceinline__ void before(uint32_t (&m)[NW], int eb)
 }
 
 template <typename TX, int S, bool kEdge, int kFull>
-__global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_kind(kFull), S, kEdge))
+__global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_kind(kFull), S))
     add_fwd_ring(const __grid_constant__ FwdArgs a, const __grid_constant__ RowPlan pl)
 {
     grid_dependency_sync();

@@ -26,44 +26,41 @@ namespace gbn {
 // Schedules.  A row of up to `cap` vectors goes to a row group of W threads
 // with KV vectors each (vector v of the row to thread v % W); a CTA of T
 // threads has G = T / W groups.  Up to 32 vectors: one a lane.  From there on
-// several a thread, so that the row reduction, its barrier and the ring's work
-// per row are shared by them: four in the forwards (rows of up to 128 vectors
-// stay in one warp), two in the backwards, which hold a column sum and a
-// weight of every element next to the row.  The widest backward holds four
-// column sums and weights and reads its row from the ring a second time
-// instead of keeping it.  A warp skips those of its KV vectors that lie past
-// the row's end.  Rows that leave many lanes of a fixed group idle (kRowFit)
-// take groups of as many warps as they fill, with four vectors a thread.
+// several a thread, which then share the row's reduction, its barrier and the
+// ring's work.  A warp skips those of its KV vectors that lie past the row's
+// end.  Rows that leave many lanes of a fixed group idle (kRowFit) take groups
+// of as many warps as they fill.
+//   Two vectors (kRow2): the backwards, which hold a column sum and a weight
+// of every element next to the row (128 registers; the widest rows take four,
+// read from the ring a second time instead of kept), and the forwards that
+// write as many 16-bit values as they read.  What bounds those is how many
+// copies are in flight: with two CTAs of two 16 KB stages an SM, 64 KB, y at
+// N = 1024 runs at 94% of the copy rate, with 128 KB at 88%.
+//   Four (kRow4): the 8-bit output and the checkpoint alone, which write less
+// and compute more (8-bit output N = 2048: 92%, with two vectors 85%).
 struct RowSched {
     int cap, W, KV, T;  // W 0: kRowFit, chosen in the launch
 };
 constexpr int kNumRowSched = 11, kRowFit = 10;
-constexpr RowSched kRowF[kNumRowSched] = {
-    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
-    {64, 32, 2, 256},  {128, 32, 4, 256}, {256, 64, 4, 256},  {512, 128, 4, 256},
-    {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
-};
-constexpr RowSched kRowB[kNumRowSched] = {
-    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
-    {64, 32, 2, 256},  {128, 64, 2, 256}, {256, 128, 2, 256}, {512, 256, 2, 256},
+constexpr RowSched kRow2[kNumRowSched] = {
+    {4, 4, 1, 256},      {8, 8, 1, 256},      {16, 16, 1, 256},   {32, 32, 1, 256},
+    {64, 32, 2, 256},    {128, 64, 2, 256},   {256, 128, 2, 256}, {512, 256, 2, 256},
     {1024, 512, 2, 512}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
 };
-// The forward that also packs the checkpoint does the most per element; two
-// vectors a thread leave it three CTAs an SM ([16384, 4096] bf16: 99 us, 108
-// with four vectors and two CTAs).
-constexpr RowSched kRowC[kNumRowSched] = {
-    {4, 4, 1, 256},    {8, 8, 1, 256},    {16, 16, 1, 256},   {32, 32, 1, 256},
-    {64, 32, 2, 256},  {128, 64, 2, 256}, {256, 128, 2, 256}, {512, 256, 2, 256},
+constexpr RowSched kRow4[kNumRowSched] = {
+    {4, 4, 1, 256},      {8, 8, 1, 256},      {16, 16, 1, 256},  {32, 32, 1, 256},
+    {64, 32, 2, 256},    {128, 32, 4, 256},   {256, 64, 4, 256}, {512, 128, 4, 256},
     {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
 };
-enum RowKind : int { kKindF = 0, kKindC = 1, kKindB = 2, kKindQ = 3 };
+// Kinds of kernels: 8-bit output or checkpoint alone; y (and checkpoint); backward.
+enum RowKind : int { kKindQ = 0, kKindY = 1, kKindB = 2 };
 constexpr int fwd_kind(int mode)
 {
-    return (mode & 3) == kModeYC ? kKindC : (mode & 3) == kModeQ ? kKindQ : kKindF;
+    return (mode & 3) == kModeY || (mode & 3) == kModeYC ? kKindY : kKindQ;
 }
 constexpr const RowSched& row_sched(int kind, int S)
 {
-    return kind == kKindB ? kRowB[S] : kind == kKindC ? kRowC[S] : kRowF[S];
+    return kind == kKindQ ? kRow4[S] : kRow2[S];
 }
 // Row groups of a CTA (kRowFit: with W threads each).
 constexpr int row_G(int kind, int S, int W = 0)
@@ -76,14 +73,11 @@ constexpr int row_G(int kind, int S, int W = 0)
 // one mask and one set of weights a thread.)
 constexpr int row_U(int kind, int S) { return row_sched(kind, S).KV == 1 ? 2 : 1; }
 // CTAs an SM holds at least (their register budget), and ring stages.
-constexpr int row_minb(int kind, int S, bool edge)
+constexpr int row_minb(int kind, int S)
 {
     const RowSched& e = row_sched(kind, S);
-    return e.T == 512    ? 1
-           : kind == kKindB ? 2
-           : e.KV == 1      ? 3
-           : e.KV == 2 && kind != kKindF ? 3
-                                         : 2;
+    if (e.T == 512) return 1;
+    return kind != kKindB && (e.KV == 1 || (e.KV == 2 && kind == kKindQ)) ? 3 : 2;
 }
 constexpr int row_stages(int kind, int S)
 {

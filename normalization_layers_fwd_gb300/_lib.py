@@ -385,20 +385,45 @@ def _raw_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# The same handle without a Stream object around it: 0.1 us instead of 2 us a call.
+# The same handles without a Stream or Device object around them.  A call on
+# one token takes the host longer than the GPU, so the checks below are written
+# for the case that passes them; what fails is left to the functions that know
+# the message.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_F32 = torch.float32
 
 
-def _call(name, device, *args):
-    fn = getattr(_handle or load(), name)
-    index = device.index
-    if index == torch.cuda.current_device():
+def _call(fn, name, index, *args):
+    """One entry point on device `index` and its current stream."""
+    if index == _current_device():
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             st = fn(*args, _raw_stream(index))
     if st != GBN_OK:
         raise GbnError(st, name)
+
+
+def _act(t, name, like=None):
+    """(t or a contiguous copy, its layout) of an activation; like: the tensor
+    it must match in shape, type and device."""
+    if like is None:
+        if t.dtype not in _DTYPES:
+            _code(t)
+        if not t.is_cuda:
+            raise ValueError("activations must be CUDA tensors")
+        if t.dim() < 1:
+            raise ValueError("activations need at least one dimension")
+    elif (t.dtype != like.dtype or t.shape != like.shape
+          or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must match in shape, dtype and device: {tuple(t.shape)} "
+                         f"{t.dtype} {t.device}, expected {tuple(like.shape)} {like.dtype} "
+                         f"{like.device}")
+    if t.is_contiguous():
+        return t, None
+    t, lay = row_layout(t)
+    return t, _lay(lay)
 
 
 def _like(t):
@@ -408,25 +433,18 @@ def _like(t):
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _act(t, name, like=None):
-    """(t or a contiguous copy, its layout, M, N) of an activation; like: the
-    tensor it must match in shape, type and device."""
-    if not t.is_cuda:
-        raise ValueError("activations must be CUDA tensors")
-    if like is None:
-        _code(t)
-        if t.dim() < 1:
-            raise ValueError("activations need at least one dimension")
-    elif t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must match in shape, dtype and device: {tuple(t.shape)} "
-                         f"{t.dtype} {t.device}, expected {tuple(like.shape)} {like.dtype} "
-                         f"{like.device}")
-    N = t.shape[-1]
-    M = t.numel() // N if N else 0
+def _like8(t, dtype):
+    """A contiguous output of t's shape in another type."""
     if t.is_contiguous():
-        return t, None, M, N
-    t, lay = row_layout(t)
-    return t, _lay(lay), M, N
+        return torch.empty_like(t, dtype=dtype)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
+def _weight(w, x, n):
+    """The weight, contiguous, of n elements on x's device."""
+    if w.get_device() != x.get_device() or w.numel() != n or not w.is_contiguous():
+        return _param(w, x, n, "w")
+    return w
 
 
 def _code8(dtype) -> int:
@@ -436,42 +454,50 @@ def _code8(dtype) -> int:
         raise TypeError(f"unsupported 8-bit dtype {dtype}: float8_e4m3fn or int8") from None
 
 
-def _scales(x, N, group):
-    """An empty tensor for x's scales: [..., ceil(N / group)], [..., 1] for rows."""
-    if group not in (0, 32, 64, 128):
+def _scale_shape(shape, group):
+    """The shape of a tensor's scales: [..., ceil(N / group)], [..., 1] for rows."""
+    if group == 0:
+        return (*shape[:-1], 1)
+    if group not in (32, 64, 128):
         raise ValueError(f"group is {group}: 0 (a scale per row), 32, 64 or 128 columns")
-    n = 1 if group == 0 else -(-N // group)
-    return torch.empty((*x.shape[:-1], n), dtype=torch.float32, device=x.device)
+    return (*shape[:-1], -(-shape[-1] // group))
 
 
 def _add_inputs(x, residual, w, s):
-    """The forwards' inputs and the stream's output."""
-    x, xl, M, N = _act(x, "x")
-    w = _param(w, x, N, "w")
-    rl = None
+    """The forwards' inputs, the stream and its output (None: the stream is x)."""
+    x, xl = _act(x, "x")
+    shape = x.shape
+    N = shape[-1]
+    M = x.numel() // N if N else 0
+    w = _weight(w, x, N)
     if residual is None:
         if s is not None:
             raise ValueError("s is an output of the addition: without a residual the stream is x")
-        return x, xl, None, None, w, x, None, M, N
-    residual, rl, _, _ = _act(residual, "residual", x)
+        return x, xl, None, None, None, w, x, None, M, N
+    residual, rl = _act(residual, "residual", x)
     if s is None:
         s = _like(x)
-    elif (s.shape != x.shape or s.dtype != x.dtype or s.device != x.device
+    elif (s.shape != shape or s.dtype != x.dtype or s.get_device() != x.get_device()
           or not s.is_contiguous()):
         raise ValueError("s must be contiguous and match x in shape, dtype and device")
-    return x, xl, residual, rl, w, s, s, M, N
+    return x, xl, residual, residual.data_ptr(), rl, w, s, s.data_ptr(), M, N
 
 
 def rmsnorm_add_fwd(x, residual, w, eps=1e-6, save_rstd=True, variant=GBN_RMS_CAST_FIRST, s=None):
     """(y, s, rstd): s = x + residual, rounded once to x's type, and y the
     RMSNorm of s (variant as in rmsnorm_fwd).  residual None: s is x.  s: a
     contiguous tensor that takes the sum; it may be x or residual itself."""
-    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
+    # residual is held here: a copy of a strided one must live until the launch
+    x, xl, residual, rp, rl, w, s, sp, M, N = _add_inputs(x, residual, w, s)
     y = _like(x)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if save_rstd else None
-    _call("rmsnorm_add_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
-          _ptr(y), _ptr(rstd), M, N, eps, _code(x), _code(w), variant)
-    return y, stream, rstd
+    rstd = rstdp = None
+    if save_rstd:
+        rstd = torch.empty(M, dtype=_F32, device=x.device)
+        rstdp = rstd.data_ptr()
+    _call((_handle or load()).rmsnorm_add_fwd, "rmsnorm_add_fwd", x.get_device(), x.data_ptr(), xl,
+          rp, rl, w.data_ptr(), sp, y.data_ptr(), rstdp, M, N, eps, _DTYPES[x.dtype], _code(w),
+          variant)
+    return y, s, rstd
 
 
 def rmsnorm_add_quant_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, group=0,
@@ -481,13 +507,18 @@ def rmsnorm_add_quant_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, g
     group of 32, 64 or 128 columns: y is q * scale.  y stays f32 up to the
     8-bit rounding, so variants 0 and 1 are the same here."""
     qt = _code8(dtype)
-    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
-    scale = _scales(x, N, group)
-    q = torch.empty(x.shape, dtype=dtype, device=x.device)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if save_rstd else None
-    _call("rmsnorm_add_quant_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
-          _ptr(q), _ptr(scale), _ptr(rstd), M, N, group, eps, _code(x), _code(w), qt, variant)
-    return q, scale, stream, rstd
+    x, xl, residual, rp, rl, w, s, sp, M, N = _add_inputs(x, residual, w, s)
+    shape, device = x.shape, x.device
+    scale = torch.empty(_scale_shape(shape, group), dtype=_F32, device=device)
+    q = _like8(x, dtype)
+    rstd = rstdp = None
+    if save_rstd:
+        rstd = torch.empty(M, dtype=_F32, device=device)
+        rstdp = rstd.data_ptr()
+    _call((_handle or load()).rmsnorm_add_quant_fwd, "rmsnorm_add_quant_fwd", x.get_device(),
+          x.data_ptr(), xl, rp, rl, w.data_ptr(), sp, q.data_ptr(), scale.data_ptr(), rstdp, M, N,
+          group, eps, _DTYPES[x.dtype], _code(w), qt, variant)
+    return q, scale, s, rstd
 
 
 def rmsnorm_add_ckpt_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, group=128,
@@ -495,15 +526,16 @@ def rmsnorm_add_ckpt_fwd(x, residual, w, eps=1e-6, dtype=torch.float8_e4m3fn, gr
     """(y, s, rstd, c, cscale): rmsnorm_add_fwd that also writes the 8-bit
     checkpoint of s (act_pack8's c and cscale) in the same pass."""
     ct = _code8(dtype)
-    x, xl, residual, rl, w, stream, out, M, N = _add_inputs(x, residual, w, s)
-    cscale = _scales(x, N, group)
-    c = torch.empty(x.shape, dtype=dtype, device=x.device)
+    x, xl, residual, rp, rl, w, s, sp, M, N = _add_inputs(x, residual, w, s)
+    shape, device = x.shape, x.device
+    cscale = torch.empty(_scale_shape(shape, group), dtype=_F32, device=device)
+    c = _like8(x, dtype)
     y = _like(x)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    _call("rmsnorm_add_ckpt_fwd", x.device, _ptr(x), xl, _ptr(residual), rl, _ptr(w), _ptr(out),
-          _ptr(y), _ptr(rstd), _ptr(c), _ptr(cscale), M, N, group, eps, _code(x), _code(w), ct,
-          variant)
-    return y, stream, rstd, c, cscale
+    rstd = torch.empty(M, dtype=_F32, device=device)
+    _call((_handle or load()).rmsnorm_add_ckpt_fwd, "rmsnorm_add_ckpt_fwd", x.get_device(),
+          x.data_ptr(), xl, rp, rl, w.data_ptr(), sp, y.data_ptr(), rstd.data_ptr(), c.data_ptr(),
+          cscale.data_ptr(), M, N, group, eps, _DTYPES[x.dtype], _code(w), ct, variant)
+    return y, s, rstd, c, cscale
 
 
 @functools.lru_cache(maxsize=4096)
@@ -514,48 +546,54 @@ def _add_ws_bytes(M, N, xt, wt, index):
     return n
 
 
-def _add_grads(dy, ds, w, rstd, need_dw, M, N):
-    """The backwards' remaining inputs and outputs."""
-    w = _param(w, dy, N, "w")
-    rstd = _param(rstd, dy, M, "rstd")
-    if rstd.dtype != torch.float32:
+def _add_grads(dy, ds, w, rstd, need_dw):
+    """The backwards' remaining inputs and outputs: (w, rstd, ds, its pointer
+    and layout, dx, dw, its pointer, the workspace, its pointer and size, M, N)."""
+    N = dy.shape[-1]
+    M = dy.numel() // N if N else 0
+    w = _weight(w, dy, N)
+    if rstd.dtype != _F32:
         raise TypeError("rstd must be float32")
-    dsl = None
+    if rstd.get_device() != dy.get_device() or rstd.numel() != M or not rstd.is_contiguous():
+        rstd = _param(rstd, dy, M, "rstd")
+    dsp = dsl = None
     if ds is not None:
-        ds, dsl, _, _ = _act(ds, "ds", dy)
+        ds, dsl = _act(ds, "ds", dy)
+        dsp = ds.data_ptr()
     dx = _like(dy)
-    dw = ws = None
+    dw = dwp = ws = wsp = None
     n = 0
     if need_dw:
-        dw = torch.empty(N, dtype=w.dtype, device=dy.device)
-        n = _add_ws_bytes(M, N, _code(dy), _code(w), dy.device.index)
-        ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
-    return w, rstd, ds, dsl, dx, dw, ws, n
+        device = dy.device
+        dw = torch.empty(N, dtype=w.dtype, device=device)
+        dwp = dw.data_ptr()
+        n = _add_ws_bytes(M, N, _DTYPES[dy.dtype], _code(w), device.index)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        wsp = ws.data_ptr()
+    return w, rstd, ds, dsp, dsl, dx, dw, dwp, ws, wsp, n, M, N
 
 
 def rmsnorm_add_bwd(s, dy, w, rstd, ds=None, need_dw=True, variant=GBN_RMS_CAST_FIRST):
     """(dx, dw): dx is the gradient of x and of the residual alike, ds (the
     gradient of s from its other readers, None for none) included.  s and rstd
     are the forward's."""
-    dy, dyl, M, N = _act(dy, "dy")
-    s, sl, _, _ = _act(s, "s", dy)
-    w, rstd, ds, dsl, dx, dw, ws, n = _add_grads(dy, ds, w, rstd, need_dw, M, N)
-    _call("rmsnorm_add_bwd", dy.device, _ptr(s), sl, _ptr(dy), dyl, _ptr(ds), dsl, _ptr(w),
-          _ptr(rstd), _ptr(dx), _ptr(dw), M, N, _code(dy), _code(w), variant, _ptr(ws), n)
+    dy, dyl = _act(dy, "dy")
+    s, sl = _act(s, "s", dy)
+    w, rstd, ds, dsp, dsl, dx, dw, dwp, ws, wsp, n, M, N = _add_grads(dy, ds, w, rstd, need_dw)
+    _call((_handle or load()).rmsnorm_add_bwd, "rmsnorm_add_bwd", dy.get_device(), s.data_ptr(), sl,
+          dy.data_ptr(), dyl, dsp, dsl, w.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dwp, M, N,
+          _DTYPES[dy.dtype], _code(w), variant, wsp, n)
     return dx, dw
 
 
-def _packed(c, cscale, group, shape, device):
+def _packed(c, cscale, group, shape, index):
     """An 8-bit tensor and its scales, checked and contiguous."""
     ct = _code8(c.dtype)
-    if not c.is_cuda or c.shape != shape or c.device != device:
-        raise ValueError(f"the 8-bit tensor must be {tuple(shape)} on {device}")
-    if group not in (0, 32, 64, 128):
-        raise ValueError(f"group is {group}: 0 (a scale per row), 32, 64 or 128 columns")
-    n = 1 if group == 0 else -(-shape[-1] // group)
-    if (cscale.shape != (*shape[:-1], n) or cscale.dtype != torch.float32
-            or cscale.device != device):
-        raise ValueError(f"the scales must be float32 {(*shape[:-1], n)} on {device}")
+    if index < 0 or c.shape != shape or c.get_device() != index:
+        raise ValueError(f"the 8-bit tensor must be {tuple(shape)} on one CUDA device")
+    want = _scale_shape(shape, group)
+    if cscale.shape != want or cscale.dtype != _F32 or cscale.get_device() != index:
+        raise ValueError(f"the scales must be float32 {want} on the 8-bit tensor's device")
     return c.contiguous(), cscale.contiguous(), ct
 
 
@@ -563,12 +601,13 @@ def rmsnorm_add_ckpt_bwd(c, cscale, dy, w, rstd, ds=None, group=128, need_dw=Tru
                          variant=GBN_RMS_CAST_FIRST):
     """(dx, dw) like rmsnorm_add_bwd, from the 8-bit checkpoint of s (c, cscale
     and group as rmsnorm_add_ckpt_fwd or act_pack8 made them) in place of s."""
-    dy, dyl, M, N = _act(dy, "dy")
-    c, cscale, ct = _packed(c, cscale, group, dy.shape, dy.device)
-    w, rstd, ds, dsl, dx, dw, ws, n = _add_grads(dy, ds, w, rstd, need_dw, M, N)
-    _call("rmsnorm_add_ckpt_bwd", dy.device, _ptr(c), _ptr(cscale), _ptr(dy), dyl, _ptr(ds), dsl,
-          _ptr(w), _ptr(rstd), _ptr(dx), _ptr(dw), M, N, group, _code(dy), _code(w), ct, variant,
-          _ptr(ws), n)
+    dy, dyl = _act(dy, "dy")
+    c, cscale, ct = _packed(c, cscale, group, dy.shape, dy.get_device())
+    w, rstd, ds, dsp, dsl, dx, dw, dwp, ws, wsp, n, M, N = _add_grads(dy, ds, w, rstd, need_dw)
+    _call((_handle or load()).rmsnorm_add_ckpt_bwd, "rmsnorm_add_ckpt_bwd", dy.get_device(),
+          c.data_ptr(), cscale.data_ptr(), dy.data_ptr(), dyl, dsp, dsl, w.data_ptr(),
+          rstd.data_ptr(), dx.data_ptr(), dwp, M, N, group, _DTYPES[dy.dtype], _code(w), ct,
+          variant, wsp, n)
     return dx, dw
 
 
@@ -576,10 +615,13 @@ def act_pack8(x, dtype=torch.float8_e4m3fn, group=128):
     """(c, cscale): x in 8 bits (float8_e4m3fn or int8) with f32 scales per row
     (group 0) or per group of 32, 64 or 128 columns; x is about c * cscale."""
     ct = _code8(dtype)
-    x, xl, M, N = _act(x, "x")
-    cscale = _scales(x, N, group)
-    c = torch.empty(x.shape, dtype=dtype, device=x.device)
-    _call("act_pack8", x.device, _ptr(x), xl, _ptr(c), _ptr(cscale), M, N, group, _code(x), ct)
+    x, xl = _act(x, "x")
+    shape, device = x.shape, x.device
+    N = shape[-1]
+    cscale = torch.empty(_scale_shape(shape, group), dtype=_F32, device=device)
+    c = _like8(x, dtype)
+    _call((_handle or load()).act_pack8, "act_pack8", device.index, x.data_ptr(), xl, c.data_ptr(),
+          cscale.data_ptr(), x.numel() // N if N else 0, N, group, _DTYPES[x.dtype], ct)
     return c, cscale
 
 
@@ -587,9 +629,12 @@ def act_unpack8(c, cscale, dtype=torch.bfloat16, group=128):
     """c * cscale in dtype: what act_pack8 (or a quantised output) stands for."""
     if c.dim() < 1:
         raise ValueError("activations need at least one dimension")
-    c, cscale, ct = _packed(c, cscale, group, c.shape, c.device)
-    x = torch.empty(c.shape, dtype=dtype, device=c.device)
-    N = c.shape[-1]
-    M = c.numel() // N if N else 0
-    _call("act_unpack8", c.device, _ptr(c), _ptr(cscale), _ptr(x), M, N, group, _code(x), ct)
+    shape, index = c.shape, c.get_device()
+    c, cscale, ct = _packed(c, cscale, group, shape, index)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}: float32, bfloat16 or float16")
+    x = torch.empty_like(c, dtype=dtype)  # c is contiguous
+    N = shape[-1]
+    _call((_handle or load()).act_unpack8, "act_unpack8", index, c.data_ptr(), cscale.data_ptr(),
+          x.data_ptr(), c.numel() // N if N else 0, N, group, _DTYPES[dtype], ct)
     return x

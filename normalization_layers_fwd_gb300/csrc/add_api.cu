@@ -61,33 +61,43 @@ gbn::Q8 q8_of(void* v, const float* scale, int type, int64_t N, int64_t group)
     return q;
 }
 
-// Whether groups fitted to the row pay (four vectors a thread, kRowFit): where
-// a fixed group's second half is nearly empty.  Measured, bf16, 2^26 elements:
-// forward N = 4097 131 -> 98 us and N = 2050 133 -> 117, but N = 5120 (5/8
-// full) 85 -> 94; backward N = 5120 113 -> 97, N = 4097 228 -> 176, but
-// N = 3001 (0.73 full) 146 -> 175; from a checkpoint N = 2050 271 -> 372.
-bool fit_pays(int kind, bool packed, int64_t nvec, int64_t cap)
-{
-    return kind != gbn::kKindB ? 16 * nvec <= 9 * cap : !packed && 8 * nvec <= 5 * cap;
-}
-
 // The vectors a row of N elements may touch: one more than N / VEC where rows
 // start inside a vector; and the first schedule that holds them (-1: none).
 int64_t row_vectors(int64_t N, int vec, bool edge)
 {
     return edge ? (N + 2 * vec - 2) / vec : N / vec;
 }
-int find_sched(int kind, bool packed, int64_t nvec)
+int find_sched(int kind, bool packed, bool edge, int64_t nvec)
 {
-    for (int s = 0; s < gbn::kRowFit; ++s) {
-        const gbn::RowSched& e = gbn::row_sched(kind, s);
-        if (nvec > e.cap) continue;
-        return nvec > 128 && nvec <= gbn::row_sched(kind, gbn::kRowFit).cap &&
-                       fit_pays(kind, packed, nvec, e.cap)
-                   ? gbn::kRowFit
-                   : s;
+    int s = 0;
+    while (s < gbn::kRowFit && nvec > gbn::row_sched(kind, s).cap) ++s;
+    if (s == gbn::kRowFit) return -1;
+    const gbn::RowSched& e = gbn::row_sched(kind, s);
+    if (nvec <= 64 || nvec > 1024) return s;
+    // Rows that do not fill their group.  Measured in us, bf16, 2^26 elements
+    // (full: the share of the group's vectors that the row has):
+    //   y: four vectors a thread below 15/16 full (N = 2560 109 -> 85) and,
+    // without a checkpoint, where rows start inside a vector (N = 1001 104 ->
+    // 94); fitted groups up to 9/16 (N = 4097 131 -> 98, N = 5120 85 -> 94).
+    //   8-bit output: fitted groups up to 9/16, from 512 vectors on up to 5/8
+    // (N = 5120 92 -> 84, but N = 2560 97 -> 104).
+    //   backward: fitted groups of four up to 5/8 (N = 5120 113 -> 97, but
+    // N = 3000 100 -> 109); of two, where rows start inside a vector, up to
+    // 9/16 (N = 2050 162 -> 146, but N = 1300 132 -> 143).
+    //   from a checkpoint: fitted groups of two (N = 2560 108 -> 91, N = 2050
+    // 248 -> 174); wider rows of four, unless they start inside a vector
+    // (N = 5120 120 -> 94).
+    const bool half = 16 * nvec <= 9 * e.cap, most = 8 * nvec <= 5 * e.cap;
+    if (kind == gbn::kKindQ)
+        return nvec > 128 && (nvec > 512 ? most : half) ? gbn::kRowFit : s;
+    if (kind == gbn::kKindY) {
+        if (16 * nvec >= 15 * e.cap && (!edge || packed)) return s;
+        return nvec > 128 && half ? gbn::kRowFit : s - 5 + gbn::kRowMore;
     }
-    return -1;
+    if (nvec <= 128) return s;
+    if (nvec > 512) return most && !(packed && edge) ? gbn::kRowFit : s;
+    if (packed) return (nvec + 63) / 64 * 32 < e.W ? gbn::kRowFit2 : s;
+    return edge ? (half ? gbn::kRowFit2 : s) : (most ? gbn::kRowFit : s);
 }
 
 // The launch's threads per row group, groups and CTAs on the device.
@@ -112,10 +122,10 @@ RowShape row_shape(int kind, int sid, int64_t nvec, int sms)
 
 // The ring kernel's launch, or false where the general kernel takes the call:
 // every tensor on a 16-byte boundary, scattered rows whole vectors on such
-// boundaries, and a schedule for the width.  groups: the scales per row that
-// the kernel finds (0: none).
+// boundaries, and a schedule for the width.  packed: the call reads or writes
+// a checkpoint; groups: the scales per row that the kernel finds (0: none).
 bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const RowSrc* in, int nt,
-               std::initializer_list<const void*> outs, int groups, int sms)
+               std::initializer_list<const void*> outs, bool packed, int groups, int sms)
 {
     const int vec = 16 / elem_bytes(xt);
     p = gbn::RowPlan{};
@@ -128,7 +138,7 @@ bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const Ro
             return false;
     }
     const int64_t nvec = row_vectors(N, vec, p.edge);
-    p.sid = find_sched(kind, in[0].row_bytes == N && kind == gbn::kKindB, nvec);
+    p.sid = find_sched(kind, packed, p.edge, nvec);
     if (p.sid < 0) return false;
     const RowShape sh = row_shape(kind, p.sid, nvec, sms);
     p.W = sh.W;
@@ -207,7 +217,8 @@ int forward(const Fwd& f, int64_t M, int64_t N, cudaStream_t stream)
     if (!f.w && gbn::pack_fast(f.xt, a))  // a checkpoint alone, of rows of whole groups
         return launch_status(gbn::launch_pack_fast(stream, f.xt, sms, a));
     gbn::RowPlan p;
-    if (!plan_rows(p, gbn::fwd_kind(mode), f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, q8.v ? q8.ng : 0, sms))
+    if (!plan_rows(p, gbn::fwd_kind(mode), f.xt, M, N, a.in, 2, {f.s, f.y, q8.v}, f.c.v != nullptr,
+                   q8.v ? q8.ng : 0, sms))
         return launch_status(gbn::launch_add_fwd_general(stream, f.xt, sms, a));
     if (!(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
     return launch_status(f.xt == gbn::kF32   ? gbn::launch_add_fwd_f32(stream, mode, a, p)
@@ -247,7 +258,7 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     if (sms <= 0) return GBN_EDEVICE;
     if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
     gbn::RowPlan p{};
-    const bool fast = M > 0 && plan_rows(p, gbn::kKindB, xt, M, N, a.in, 3, {dx}, 0, sms);
+    const bool fast = M > 0 && plan_rows(p, gbn::kKindB, xt, M, N, a.in, 3, {dx}, cscale != nullptr, 0, sms);
     if (fast && !(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
     const int64_t P = M == 0 ? 0 : fast ? p.grid : gbn::add_bwd_general_rows(M, N, sms);
     if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
@@ -286,7 +297,7 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
     const int64_t nvec = row_vectors(N, vec, edge);
     int64_t P = add_bwd_general_rows(M, N, sms);
     for (const bool packed : {false, true}) {
-        const int sid = find_sched(kKindB, packed, nvec);
+        const int sid = find_sched(kKindB, packed, edge, nvec);
         if (sid < 0) continue;
         const RowShape sh = row_shape(kKindB, sid, nvec, sms);
         const int64_t blocks = (M + sh.R - 1) / sh.R, grid = blocks < sh.ctas ? blocks : sh.ctas;

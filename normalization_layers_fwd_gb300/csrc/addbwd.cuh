@@ -1,6 +1,17 @@
 // addbwd.cuh -- the ring kernel of the residual-stream backwards: dx (with
 // the stream's own gradient ds added) and the partial column sums of dw from
 // the stream s, or from its 8-bit checkpoint.  addbwd_*.cu instantiate it.
+//
+// One pass over s (or its codes), dy and ds.  xhat and dn are computed, enter
+// the row's sum of dn xhat and the column sums, and after the row reduction
+// give dx; they are kept in registers where those suffice and computed a
+// second time elsewhere.  A row's rstd and its groups' scales come a row block
+// ahead (fed through the ring instead, as two more copies a block, they cost
+// 30%).  Measured (bf16, of measured copy bandwidth, graph of passes):
+// [16384, 4096] 85 us, 0.93; from the checkpoint 83 us, 0.83, bound by the
+// instructions that unpack and scale the codes (its bytes take 69 us); rows
+// that start inside a vector 0.55 to 0.75.  Three CTAs an SM at 80 registers,
+// reading the row from the ring twice, took 107 us instead of 85.
 #pragma once
 
 #include "rowring.cuh"
@@ -154,7 +165,7 @@ __global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
         };
         // xhat and dn are kept over the reduction where they fit the registers
         // (8-bit codes take few), and computed again elsewhere
-        constexpr bool kKeep = kPacked && !kEdge && !kLean;
+                constexpr bool kKeep = kPacked && !kEdge && !kLean;
         f2 xk[kKeep ? U : 1][kKeep ? KV : 1][P], dk[kKeep ? U : 1][kKeep ? KV : 1][P];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -259,8 +270,10 @@ cudaError_t bwd_launch(cudaStream_t st, int mode, const BwdArgs& a, const RowPla
     auto go = [&](auto s_, auto edge_, auto mode_) {
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
-        ring_attributes<add_bwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
+        if constexpr (row_takes(kKindB, S)) {
+            ring_attributes<add_bwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
+            launch_pdl(add_bwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
+        }
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -1,9 +1,17 @@
 // addfwd.cuh -- the ring kernel of the residual-stream forwards: s = x + res,
 // its RMSNorm in x's type or in 8 bits, the 8-bit checkpoint of s, and (mode
-// kModeC) the checkpoint alone.  One pass: a thread adds and rounds its
-// vectors of s and keeps them, packed, over the row reduction; the maxima for
-// the 8-bit scales go with it (the output's largest magnitude is r times
-// that of w s, so it needs no second walk).  addfwd_*.cu instantiate it.
+// kModeC) the checkpoint alone.  addfwd_*.cu instantiate it.
+//
+// One pass: a thread adds and rounds its vectors of s and keeps them, packed,
+// over the row reduction; the maxima for the 8-bit scales go with it (the
+// output's largest magnitude is r times that of w s, so it needs no second
+// walk).  Everything read is read once and everything written once, so HBM
+// bounds it.  Measured (bf16, of measured copy bandwidth, graph of passes):
+// y [65536, 1024] 84 us, 0.94; y [16384, 4096] 88 us, 0.90; 8-bit output
+// [16384, 4096] 76 us, 0.92; y with its checkpoint 100 us, 0.89.
+// Rows that start inside a vector (odd N) pay for their masked ends and, with
+// groups, for maxima that meet in shared memory: y N = 3001 0.90, 8-bit output
+// 0.47, where the warps' instructions bound it.
 #pragma once
 
 #include "rowring.cuh"
@@ -300,8 +308,10 @@ cudaError_t fwd_launch(cudaStream_t st, int mode, const FwdArgs& a, const RowPla
     auto go = [&](auto s_, auto edge_, auto mode_) {
         constexpr int S = decltype(s_)::value, kMode = decltype(mode_)::value;
         constexpr bool kEdge = decltype(edge_)::value;
-        ring_attributes<add_fwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
-        launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
+        if constexpr (row_takes(fwd_kind(kMode), S)) {
+            ring_attributes<add_fwd_ring<TX, S, kEdge, kMode>>(kMaxSmem);
+            launch_pdl(add_fwd_ring<TX, S, kEdge, kMode>, p.grid, p.W * p.G, p.smem, st, a, p);
+        }
     };
     auto modes = [&](auto s_, auto edge_) {
         using std::integral_constant;

@@ -41,19 +41,25 @@ namespace gbn {
 struct RowSched {
     int cap, W, KV, T;  // W 0: kRowFit, chosen in the launch
 };
-constexpr int kNumRowSched = 11, kRowFit = 10;
+constexpr int kNumRowSched = 16, kRowFit = 10, kRowFit2 = 11, kRowMore = 12;
 constexpr RowSched kRow2[kNumRowSched] = {
     {4, 4, 1, 256},      {8, 8, 1, 256},      {16, 16, 1, 256},   {32, 32, 1, 256},
     {64, 32, 2, 256},    {128, 64, 2, 256},   {256, 128, 2, 256}, {512, 256, 2, 256},
-    {1024, 512, 2, 512}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
+    {1024, 512, 2, 512}, {2048, 512, 4, 512}, {1024, 0, 4, 256},  {512, 0, 2, 256},
+    {128, 32, 4, 256},   {256, 64, 4, 256},   {512, 128, 4, 256}, {1024, 256, 4, 256},
 };
 constexpr RowSched kRow4[kNumRowSched] = {
     {4, 4, 1, 256},      {8, 8, 1, 256},      {16, 16, 1, 256},  {32, 32, 1, 256},
     {64, 32, 2, 256},    {128, 32, 4, 256},   {256, 64, 4, 256}, {512, 128, 4, 256},
-    {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256},
+    {1024, 256, 4, 256}, {2048, 512, 4, 512}, {1024, 0, 4, 256}, {512, 0, 2, 256},
 };
 // Kinds of kernels: 8-bit output or checkpoint alone; y (and checkpoint); backward.
 enum RowKind : int { kKindQ = 0, kKindY = 1, kKindB = 2 };
+// Whether kernels of a kind take schedule S (the others are not built).
+constexpr bool row_takes(int kind, int S)
+{
+    return S <= kRowFit || (S == kRowFit2 ? kind == kKindB : kind == kKindY);
+}
 constexpr int fwd_kind(int mode)
 {
     return (mode & 3) == kModeY || (mode & 3) == kModeYC ? kKindY : kKindQ;
@@ -207,7 +213,8 @@ __device__ __forceinline__ void row_ring(const RowSrc (&in)[NT], const RowPlan& 
             __syncthreads();
         }
         if (!body(b, slot, alive)) __syncthreads();
-        if (threadIdx.x < 32 && alive && k + pl.stages < K) {
+        // one answer for warp 0: its lanes issue together
+        if (threadIdx.x < 32 && __all_sync(0xffffffffu, alive) && k + pl.stages < K) {
             fence_proxy_async();
             row_issue(in, pl, M, dsm, b + (int64_t)pl.stages * gridDim.x, st);
         }
@@ -506,6 +513,11 @@ inline bool with_row_sched(int sid, F&& f)
         case 8: f(std::integral_constant<int, 8>{}); return true;
         case 9: f(std::integral_constant<int, 9>{}); return true;
         case 10: f(std::integral_constant<int, 10>{}); return true;
+        case 11: f(std::integral_constant<int, 11>{}); return true;
+        case 12: f(std::integral_constant<int, 12>{}); return true;
+        case 13: f(std::integral_constant<int, 13>{}); return true;
+        case 14: f(std::integral_constant<int, 14>{}); return true;
+        case 15: f(std::integral_constant<int, 15>{}); return true;
         default: return false;
     }
 }

@@ -403,3 +403,16 @@ def test_offsets_past_32_bits():
     dx, dw = _lib.rmsnorm_add_bwd(s, s, w, rstd, s, variant=1)
     xh = ref.d(s[-tail:]) * ref.d(rstd[-tail:])[:, None]
     ref.check_gradients(dx[-tail:], None, xh, s[-tail:], s[-tail:], w, rstd[-tail:], 1, False)
+
+
+@pytest.mark.parametrize("M,N", [(300, 512), (41, 1001), (3, 20000)])
+def test_gradient_in_place_of_the_streams(M, N):
+    """dx may take the memory of ds."""
+    lib = _lib.load()
+    x, res, w, dy, ds = inputs(42, M, N)
+    _, s, rstd = _lib.rmsnorm_add_fwd(x, res, w, EPS, variant=1)
+    want, _ = _lib.rmsnorm_add_bwd(s, dy, w, rstd, ds, need_dw=False, variant=1)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert lib.rmsnorm_add_bwd(p(s), None, p(dy), None, p(ds), None, p(w), p(rstd), p(ds), None, M,
+                               N, 1, 0, 1, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    ref.same("dx", ds, want)

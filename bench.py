@@ -67,11 +67,16 @@ def measured_peak():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# What the sweep's kernels and their launches are made from.
+SWEEP_SOURCES = ("api.cu", "colsum.cu", "common.cuh", "ctx_cache.h", "dyt.cu", "internal.h",
+                 "layernorm.cu", "rmsnorm.cu", "rmsnorm.cuh", "rmsnorm_bwd.cu", "static_ws.cu")
+
+
 def source_hash():
-    """Hash of the kernel sources (ncu counters are valid only for this hash)."""
+    """Hash of the sweep's kernel sources (ncu counters are valid only for this hash)."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "normalization_layers_fwd_gb300", "csrc")
-    for name in sorted(os.listdir(d)):
+    for name in SWEEP_SOURCES:
         with open(os.path.join(d, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]

@@ -67,37 +67,51 @@ int64_t row_vectors(int64_t N, int vec, bool edge)
 {
     return edge ? (N + 2 * vec - 2) / vec : N / vec;
 }
-int find_sched(int kind, bool packed, bool edge, int64_t nvec)
+// Whether every CTA of a backward takes rows enough (about 16) that the cost
+// of its row counts, and not the first row's latency.
+bool many_rows(int64_t M, int sms) { return M >= 32LL * sms; }
+
+// The schedule of a row of nvec vectors (-1: too wide): the first whose groups
+// hold it, or one for rows that do not fill those.  packed: the call reads or
+// writes a checkpoint; edge: rows start inside a vector.  In us, bf16, 2^26
+// elements a call, groups as they would be -> as they are:
+//   y: two vectors a thread where the row fills them (N = 1024 90 -> 84), four
+// elsewhere (N = 2560 109 -> 85), also where rows start inside a vector and no
+// checkpoint is written (N = 1001 104 -> 94).
+//   8-bit output, checkpoint alone: four.
+//   backward: as y (N = 2560 99 -> 90, N = 3001 133 -> 110, N = 1001 107 -> 100).
+//   backward from a checkpoint: four, given many rows (N = 4096 83 -> 78, but
+// [64, 8192] 8.6 -> 10.3), and two where rows start inside a vector (N = 1001
+// 172 -> 131) or leave much of the group empty.
+//   Groups fitted to the row, kRowFit (four vectors a thread) and kRowFit2
+// (two): where a fixed group would be about half empty: y N = 4097 131 -> 94,
+// backward N = 4097 228 -> 143, from a checkpoint N = 2560 108 -> 91 and
+// N = 2050 247 -> 174, 8-bit output N = 5120 92 -> 84; not at 5/8 (y N = 5120
+// 94 fitted, 85 fixed).
+int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
 {
     int s = 0;
     while (s < gbn::kRowFit && nvec > gbn::row_sched(kind, s).cap) ++s;
     if (s == gbn::kRowFit) return -1;
     const gbn::RowSched& e = gbn::row_sched(kind, s);
     if (nvec <= 64 || nvec > 1024) return s;
-    // Rows that do not fill their group.  Measured in us, bf16, 2^26 elements
-    // (full: the share of the group's vectors that the row has):
-    //   y: four vectors a thread below 15/16 full (N = 2560 109 -> 85) and,
-    // without a checkpoint, where rows start inside a vector (N = 1001 104 ->
-    // 94); fitted groups up to 9/16 (N = 4097 131 -> 98, N = 5120 85 -> 94).
-    //   8-bit output: fitted groups up to 9/16, from 512 vectors on up to 5/8
-    // (N = 5120 92 -> 84, but N = 2560 97 -> 104).
-    //   backward: fitted groups of four up to 5/8 (N = 5120 113 -> 97, but
-    // N = 3000 100 -> 109); of two, where rows start inside a vector, up to
-    // 9/16 (N = 2050 162 -> 146, but N = 1300 132 -> 143).
-    //   from a checkpoint: fitted groups of two (N = 2560 108 -> 91, N = 2050
-    // 248 -> 174); wider rows of four, unless they start inside a vector
-    // (N = 5120 120 -> 94).
     const bool half = 16 * nvec <= 9 * e.cap, most = 8 * nvec <= 5 * e.cap;
-    if (kind == gbn::kKindQ)
-        return nvec > 128 && (nvec > 512 ? most : half) ? gbn::kRowFit : s;
+    const bool full = 16 * nvec >= 15 * e.cap;
+    const int four = s - 5 + gbn::kRowMore;  // the same groups, four vectors a thread
+    const bool wide = nvec > 128;
+    if (kind == gbn::kKindQ) return wide && (nvec > 512 ? most : half) ? gbn::kRowFit : s;
     if (kind == gbn::kKindY) {
-        if (16 * nvec >= 15 * e.cap && (!edge || packed)) return s;
-        return nvec > 128 && half ? gbn::kRowFit : s - 5 + gbn::kRowMore;
+        if (full && (!edge || packed)) return s;
+        return wide && half ? gbn::kRowFit : four;
     }
-    if (nvec <= 128) return s;
-    if (nvec > 512) return most && !(packed && edge) ? gbn::kRowFit : s;
-    if (packed) return (nvec + 63) / 64 * 32 < e.W ? gbn::kRowFit2 : s;
-    return edge ? (half ? gbn::kRowFit2 : s) : (most ? gbn::kRowFit : s);
+    if (!packed) {  // backward from here on
+        if (full && !edge) return s;
+        if (wide && half) return edge && nvec <= 512 ? gbn::kRowFit2 : gbn::kRowFit;
+        return four;
+    }
+    if (!edge && many && !most) return four;
+    if (wide && nvec <= 512) return (nvec + 63) / 64 * 32 < e.W ? gbn::kRowFit2 : s;
+    return wide && !edge && most ? gbn::kRowFit : s;
 }
 
 // The launch's threads per row group, groups and CTAs on the device.
@@ -138,7 +152,7 @@ bool plan_rows(gbn::RowPlan& p, int kind, int xt, int64_t M, int64_t N, const Ro
             return false;
     }
     const int64_t nvec = row_vectors(N, vec, p.edge);
-    p.sid = find_sched(kind, packed, p.edge, nvec);
+    p.sid = find_sched(kind, packed, p.edge, nvec, many_rows(M, sms));
     if (p.sid < 0) return false;
     const RowShape sh = row_shape(kind, p.sid, nvec, sms);
     p.W = sh.W;
@@ -297,7 +311,7 @@ size_t add_bwd_workspace_bytes(int64_t M, int64_t N, int xt, int sms)
     const int64_t nvec = row_vectors(N, vec, edge);
     int64_t P = add_bwd_general_rows(M, N, sms);
     for (const bool packed : {false, true}) {
-        const int sid = find_sched(kKindB, packed, edge, nvec);
+        const int sid = find_sched(kKindB, packed, edge, nvec, many_rows(M, sms));
         if (sid < 0) continue;
         const RowShape sh = row_shape(kKindB, sid, nvec, sms);
         const int64_t blocks = (M + sh.R - 1) / sh.R, grid = blocks < sh.ctas ? blocks : sh.ctas;

@@ -30,19 +30,22 @@ namespace gbn {
 // ring's work.  A warp skips those of its KV vectors that lie past the row's
 // end.  Rows that leave many lanes of a fixed group idle (kRowFit) take groups
 // of as many warps as they fill.
-//   Two vectors (kRow2): the backwards, which hold a column sum and a weight
-// of every element next to the row (128 registers; the widest rows take four,
-// read from the ring a second time instead of kept), and the forwards that
-// write as many 16-bit values as they read.  What bounds those is how many
-// copies are in flight: with two CTAs of two 16 KB stages an SM, 64 KB, y at
-// N = 1024 runs at 94% of the copy rate, with 128 KB at 88%.
-//   Four (kRow4): the 8-bit output and the checkpoint alone, which write less
-// and compute more (8-bit output N = 2048: 92%, with two vectors 85%).
+//   Two vectors (kRow2): the forwards that write as many 16-bit values as they
+// read, and the backwards, which hold a column sum and a weight of every
+// element next to the row.  What bounds y is how many copies are in flight:
+// with two CTAs of two 16 KB stages an SM, 64 KB, N = 1024 runs at 94% of the
+// copy rate, with 128 KB at 88%.
+//   Four (kRow4, and kRow2 from kRowMore on): the 8-bit output and the
+// checkpoint alone, which write less and compute more (8-bit output N = 2048:
+// 92%, with two vectors 85%); rows that do not fill their group; and the
+// backward from a checkpoint.  A backward with four reads its row from the
+// ring a second time instead of keeping it (128 registers hold the sums, the
+// weights and little more).
 struct RowSched {
     int cap, W, KV, T;  // W 0: kRowFit, chosen in the launch
 };
 constexpr int kNumRowSched = 16, kRowFit = 10, kRowFit2 = 11, kRowMore = 12;
-constexpr RowSched kRow2[kNumRowSched] = {
+constexpr RowSched kRow2[kNumRowSched] = {  // 9 and kRowFit: four
     {4, 4, 1, 256},      {8, 8, 1, 256},      {16, 16, 1, 256},   {32, 32, 1, 256},
     {64, 32, 2, 256},    {128, 64, 2, 256},   {256, 128, 2, 256}, {512, 256, 2, 256},
     {1024, 512, 2, 512}, {2048, 512, 4, 512}, {1024, 0, 4, 256},  {512, 0, 2, 256},
@@ -58,7 +61,7 @@ enum RowKind : int { kKindQ = 0, kKindY = 1, kKindB = 2 };
 // Whether kernels of a kind take schedule S (the others are not built).
 constexpr bool row_takes(int kind, int S)
 {
-    return S <= kRowFit || (S == kRowFit2 ? kind == kKindB : kind == kKindY);
+    return S <= kRowFit || (S == kRowFit2 ? kind == kKindB : kind != kKindQ);
 }
 constexpr int fwd_kind(int mode)
 {

@@ -85,8 +85,8 @@ bool many_rows(int64_t M, int sms) { return M >= 32LL * sms; }
 // 172 -> 131) or leave much of the group empty.
 //   Groups fitted to the row, kRowFit (four vectors a thread) and kRowFit2
 // (two): where a fixed group would be about half empty: y N = 4097 131 -> 94,
-// backward N = 4097 228 -> 143, from a checkpoint N = 2560 108 -> 91 and
-// N = 2050 247 -> 174, 8-bit output N = 5120 92 -> 84; not at 5/8 (y N = 5120
+// backward N = 4097 228 -> 143, from a checkpoint N = 2560 108 -> 91, N = 2050
+// 247 -> 174 and N = 4097 248 -> 219, 8-bit output N = 5120 92 -> 84; not at 5/8 (y N = 5120
 // 94 fitted, 85 fixed).
 int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
 {
@@ -111,7 +111,7 @@ int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
     }
     if (!edge && many && !most) return four;
     if (wide && nvec <= 512) return (nvec + 63) / 64 * 32 < e.W ? gbn::kRowFit2 : s;
-    return wide && !edge && most ? gbn::kRowFit : s;
+    return wide && (edge ? half : most) ? gbn::kRowFit : s;
 }
 
 // The launch's threads per row group, groups and CTAs on the device.
@@ -288,7 +288,7 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     a.variant = variant;
     if (M > 0) {
         const int mode = cscale ? (ct == gbn::kInt8 ? gbn::kBwdInt8 : gbn::kBwdC)
-                         : variant == GBN_RMS_CAST_FIRST ? gbn::kBwdCast
+                         : variant == GBN_RMS_CAST_FIRST ? (wt == xt ? gbn::kBwdCast16 : gbn::kBwdCast)
                                                          : gbn::kBwdS;
         const cudaError_t rc = !fast               ? gbn::launch_add_bwd_general(stream, xt, P, a)
                                : xt == gbn::kF32 ? gbn::launch_add_bwd_f32(stream, mode, a, p)

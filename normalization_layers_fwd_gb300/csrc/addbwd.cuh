@@ -8,9 +8,10 @@
 // second time elsewhere.  A row's rstd and its groups' scales come a row block
 // ahead (fed through the ring instead, as two more copies a block, they cost
 // 30%).  Measured (bf16, of measured copy bandwidth, graph of passes):
-// [16384, 4096] 85 us, 0.93; from the checkpoint 83 us, 0.83, bound by the
-// instructions that unpack and scale the codes (its bytes take 69 us); rows
-// that start inside a vector 0.55 to 0.75.  Three CTAs an SM at 80 registers,
+// [16384, 4096] 85 us, 0.93, in every expression (expression 0 with a 16-bit
+// weight multiplies packed pairs: 92 us with f32 pairs rounded after); from the
+// checkpoint 78 us, 0.89, where unpacking and scaling the codes bounds it; rows
+// that start inside a vector 0.55 to 0.8.  Three CTAs an SM at 80 registers,
 // reading the row from the ring twice, took 107 us instead of 85.
 #pragma once
 
@@ -27,7 +28,8 @@ __global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
     constexpr int kW = kRow2[S].W, KV = kRow2[S].KV, U = row_U(kKindB, S);
     constexpr int kG = row_G(kKindB, S), kLanes = kW ? kW : 256;
     constexpr int VEC = Vec<TX>::kN, P = VEC / 2, E = (int)sizeof(TX);
-    constexpr bool kPacked = kMode >= kBwdC, kCast = kMode == kBwdCast, kLean = KV > 2;
+    constexpr bool kPacked = kMode == kBwdC || kMode == kBwdInt8, kLean = KV > 2;
+    constexpr bool kCast = kMode == kBwdCast, kCast16 = kMode == kBwdCast16;
     constexpr int kType = kMode == kBwdInt8 ? kInt8 : kE4M3;
     // words of a thread's vector of s: activations, or 8-bit codes
     constexpr int NS = kPacked ? VEC / 4 : 4, VS = kPacked ? VEC : 16, ES = kPacked ? 1 : E;
@@ -45,12 +47,19 @@ __global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
     const Cols<VEC, kW, KV, kEdge> cols(l, W, kEdge ? (int)(row * N % VEC) : 0, N);
     f2 wf[KV][P], acc[KV][P];
     load_weights<VEC, kW, KV, kEdge>(wf, cols, a.w, a.wt, a.variant == 2);
+    // kCast16 holds the weights as packed pairs: they multiply 16-bit values,
+    // and the products are rounded once, as the expression says
+    uint32_t wp[KV][P];
+    if constexpr (kCast16) {
+#pragma unroll
+        for (int j = 0; j < KV; ++j)
+#pragma unroll
+            for (int p = 0; p < P; ++p) wp[j][p] = P16<TX>::from_f2(wf[j][p]);
+    }
 #pragma unroll
     for (int j = 0; j < KV; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) acc[j][p] = splat2(0.f);
-    // expression 0 with a weight of x's type rounds each term of dw
-    const bool round_terms = kCast && a.wt == dtype_code<TX>();
     int64_t at = row * N - cols.first + l * VEC;
     const int64_t row_step = (int64_t)gridDim.x * R, at_step = row_step * N;
     const uint32_t so0 = pl.off[0] + row_off(a.in[0], kPacked ? 0 : row - g, g) -
@@ -156,7 +165,13 @@ __global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
 #pragma unroll
                 for (int p = 0; p < P; ++p) xh[p] = mul2(xh[p], splat2(rs[u]));
             }
-            unpack2<TX>(dyp[u][j], dv);
+            if constexpr (!kCast16) unpack2<TX>(dyp[u][j], dv);
+            if constexpr (kCast16) {
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    dn[p] = P16<TX>::to_f2(P16<TX>::mul(word(dyp[u][j], p), wp[j][p]));
+                return;
+            }
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 dn[p] = mul2(dv[p], wf[j][p]);
@@ -178,17 +193,22 @@ __global__ void __launch_bounds__(kRow2[S].T, row_minb(kKindB, S))
                 f2 dv[P];
                 terms(u, j, xh, dn, dv);
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    q = fma2(dn[p], xh[p], q);
-                    if constexpr (kCast) {
-                        // the term dy rx(xhat): its product is exact in float32, rounded to
-                        // x's type when the weight has that type
-                        f2 t = mul2(dv[p], round2<TX>(xh[p]));
-                        if (round_terms) t = round2<TX>(t);
-                        acc[j][p] = add2(acc[j][p], t);
-                    } else {
-                        acc[j][p] = fma2(dv[p], xh[p], acc[j][p]);
-                    }
+                for (int p = 0; p < P; ++p) q = fma2(dn[p], xh[p], q);
+                // expression 0's term is dy rx(xhat): the exact product, or
+                // (kCast16) rounded to x's type
+                if constexpr (kCast16) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        acc[j][p] = add2(acc[j][p],
+                                         P16<TX>::to_f2(P16<TX>::mul(word(dyp[u][j], p),
+                                                                     P16<TX>::from_f2(xh[p]))));
+                } else if constexpr (kCast) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        acc[j][p] = fma2(dv[p], round2<TX>(xh[p]), acc[j][p]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < P; ++p) acc[j][p] = fma2(dv[p], xh[p], acc[j][p]);
                 }
             }
             sum[u] = lo2(q) + hi2(q);
@@ -283,6 +303,8 @@ cudaError_t bwd_launch(cudaStream_t st, int mode, const BwdArgs& a, const RowPla
             go(s_, edge_, integral_constant<int, kBwdInt8>{});
         else if (mode == kBwdCast && is16<TX>())
             go(s_, edge_, integral_constant<int, is16<TX>() ? kBwdCast : kBwdS>{});
+        else if (mode == kBwdCast16 && is16<TX>())
+            go(s_, edge_, integral_constant<int, is16<TX>() ? kBwdCast16 : kBwdS>{});
         else
             go(s_, edge_, integral_constant<int, kBwdS>{});
     };

@@ -251,16 +251,33 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
                 f2 sv[P];
                 unpack2<TX>(sp[u][j], sv);
                 if constexpr (kMode == kModeY || kMode == kModeYC) {
-                    f2 o[P];
-                    if (is16<TX>() && a.variant == 0) {
+                    uint4 o;
+                    f2 f[P];
+                    if constexpr (is16<TX>()) {
+                        if (a.variant != 0) {
 #pragma unroll
-                        for (int p = 0; p < P; ++p)  // n = rx(s r), y = rx(w n)
-                            o[p] = mul2(wf[j][p], round2<TX>(mul2(sv[p], r2)));
+                            for (int p = 0; p < P; ++p) f[p] = mul2(wf[j][p], mul2(sv[p], r2));
+                            o = pack2<TX>(f);
+                        } else if (a.wt == dtype_code<TX>()) {
+                            // n = rx(s r), y = rx(w n): a product of 16-bit values, rounded once
+                            uint32_t h[4];
+#pragma unroll
+                            for (int p = 0; p < P; ++p)
+                                h[p] = P16<TX>::mul(P16<TX>::from_f2(wf[j][p]),
+                                                    P16<TX>::from_f2(mul2(sv[p], r2)));
+                            o = make_uint4(h[0], h[1], h[2], h[3]);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < P; ++p)
+                                f[p] = mul2(wf[j][p], round2<TX>(mul2(sv[p], r2)));
+                            o = pack2<TX>(f);
+                        }
                     } else {
 #pragma unroll
-                        for (int p = 0; p < P; ++p) o[p] = mul2(wf[j][p], mul2(sv[p], r2));
+                        for (int p = 0; p < P; ++p) f[p] = mul2(wf[j][p], mul2(sv[p], r2));
+                        o = pack2<TX>(f);
                     }
-                    st_vec<TX>(static_cast<TX*>(a.y) + atu + j * W * VEC, pack2<TX>(o), ok,
+                    st_vec<TX>(static_cast<TX*>(a.y) + atu + j * W * VEC, o, ok,
                                cols.cut(j), cols.em[j]);
                 }
                 if constexpr (kMax) {

@@ -87,7 +87,8 @@ struct RowPlan {
 // One instance set per activation type (addfwd_*.cu, addbwd_*.cu).
 // The 8-bit modes come once per 8-bit type: + kModeInt8.
 enum FwdMode : int { kModeY = 0, kModeQ = 1, kModeYC = 2, kModeC = 3, kModeInt8 = 4 };
-enum BwdMode : int { kBwdS = 0, kBwdCast = 1, kBwdC = 2, kBwdInt8 = 3 };
+// kBwdCast: expression 0's rounding points, kBwdCast16 with a weight of x's type.
+enum BwdMode : int { kBwdS = 0, kBwdCast = 1, kBwdC = 2, kBwdInt8 = 3, kBwdCast16 = 4 };
 cudaError_t launch_add_fwd_bf16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_fwd_f16(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);
 cudaError_t launch_add_fwd_f32(cudaStream_t st, int mode, const FwdArgs& a, const RowPlan& p);

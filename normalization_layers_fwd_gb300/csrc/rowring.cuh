@@ -298,6 +298,12 @@ __device__ __forceinline__ void ld_vec8(uint32_t (&v)[VEC / 4], const unsigned c
     if (cut) mask_words<VEC>(v, em);
 }
 
+// Word p of a vector.
+__device__ __forceinline__ uint32_t word(const uint4& v, int p)
+{
+    return p == 0 ? v.x : p == 1 ? v.y : p == 2 ? v.z : v.w;
+}
+
 // Store a vector of activations; cut: the elements in the mask.
 template <typename TX>
 __device__ __forceinline__ void st_vec(TX* p, const uint4& v, bool ok, bool cut, uint32_t em)

@@ -1,6 +1,7 @@
 """GB300-native row-normalization layers: DyT, LayerNorm and Llama-style
-RMSNorm, forward and backward, as hand-written CUDA kernels for sm_103a
-behind a C ABI (include/gbnorm.h, libgbnorm.so).
+RMSNorm, forward and backward, RMSNorm with the residual's addition, its 8-bit
+output and 8-bit activation checkpoints, as hand-written CUDA kernels for
+sm_103a behind a C ABI (include/gbnorm.h, libgbnorm.so).
 
     from normalization_layers_fwd_gb300 import dyt_fwd, dyt_bwd, ...   # C-ABI names
     from normalization_layers_fwd_gb300.functional import rms_norm      # autograd

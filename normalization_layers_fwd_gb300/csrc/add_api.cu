@@ -86,7 +86,8 @@ bool many_rows(int64_t M, int sms) { return M >= 32LL * sms; }
 //   Groups fitted to the row, kRowFit (four vectors a thread) and kRowFit2
 // (two): where a fixed group would be about half empty: y N = 4097 131 -> 94,
 // backward N = 4097 228 -> 143, from a checkpoint N = 2560 108 -> 91, N = 2050
-// 247 -> 174 and N = 4097 248 -> 219, 8-bit output N = 5120 92 -> 84; not at 5/8 (y N = 5120
+// 247 -> 174 and N = 4097 248 -> 219, 8-bit output N = 5120 92 -> 84 and N = 2560
+// 98 -> 87; not at 5/8 (y N = 5120
 // 94 fitted, 85 fixed).
 int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
 {
@@ -99,7 +100,11 @@ int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
     const bool full = 16 * nvec >= 15 * e.cap;
     const int four = s - 5 + gbn::kRowMore;  // the same groups, four vectors a thread
     const bool wide = nvec > 128;
-    if (kind == gbn::kKindQ) return wide && (nvec > 512 ? most : half) ? gbn::kRowFit : s;
+    if (kind == gbn::kKindQ) {
+        if (!wide) return s;
+        if (nvec > 512) return most ? gbn::kRowFit : s;
+        return most && !edge && !packed ? gbn::kRowFit2 : half ? gbn::kRowFit : s;
+    }
     if (kind == gbn::kKindY) {
         if (full && (!edge || packed)) return s;
         return wide && half ? gbn::kRowFit : four;

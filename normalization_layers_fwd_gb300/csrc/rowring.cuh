@@ -61,7 +61,7 @@ enum RowKind : int { kKindQ = 0, kKindY = 1, kKindB = 2 };
 // Whether kernels of a kind take schedule S (the others are not built).
 constexpr bool row_takes(int kind, int S)
 {
-    return S <= kRowFit || (S == kRowFit2 ? kind == kKindB : kind != kKindQ);
+    return S <= kRowFit || (S == kRowFit2 ? kind != kKindY : kind != kKindQ);
 }
 constexpr int fwd_kind(int mode)
 {

@@ -139,7 +139,9 @@ def add_rms_norm(x, residual, weight, eps=1e-6, variant=_lib.GBN_RMS_CAST_FIRST,
     RMSNorm of s.  The backward adds the gradient that reaches s from its
     other readers in the same pass; x and residual get the same gradient.
     checkpoint and group as in dyt: s is kept in 8 bits, so the stream itself
-    need not live until the backward."""
+    need not live until the backward.  (Without a residual: rms_norm.)"""
+    if residual is None:
+        raise ValueError("residual is required: rms_norm is the norm without one")
     return _AddRMSNorm.apply(x, residual, weight, eps, variant, checkpoint, group)
 
 

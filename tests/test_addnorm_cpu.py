@@ -168,3 +168,14 @@ def test_binding_refuses_before_the_library(lib):
         _lib.act_pack8(x, torch.uint8)
     with pytest.raises(TypeError):
         _lib.rmsnorm_add_quant_fwd(x, x, w, dtype=torch.float8_e5m2)
+
+
+def test_wrappers_refuse():
+    from normalization_layers_fwd_gb300 import functional as F
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    with pytest.raises(ValueError, match="residual"):
+        F.add_rms_norm(x, None, w)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        F.add_rms_norm_quant(x.requires_grad_(), x, w)
+    with pytest.raises(ValueError):
+        F.rms_norm(x, w, checkpoint=torch.int8)

@@ -79,16 +79,16 @@ bool many_rows(int64_t M, int sms) { return M >= 32LL * sms; }
 // elsewhere (N = 2560 109 -> 85), also where rows start inside a vector and no
 // checkpoint is written (N = 1001 104 -> 94).
 //   8-bit output, checkpoint alone: four.
-//   backward: as y (N = 2560 99 -> 90, N = 3001 133 -> 110, N = 1001 107 -> 100).
+//   backward: as y, given many rows (N = 2560 99 -> 90, N = 3001 133 -> 110,
+// N = 1001 107 -> 100, but [4097, 1001] 14.7 -> 19.1).
 //   backward from a checkpoint: four, given many rows (N = 4096 83 -> 78, but
 // [64, 8192] 8.6 -> 10.3), and two where rows start inside a vector (N = 1001
 // 172 -> 131) or leave much of the group empty.
 //   Groups fitted to the row, kRowFit (four vectors a thread) and kRowFit2
 // (two): where a fixed group would be about half empty: y N = 4097 131 -> 94,
 // backward N = 4097 228 -> 143, from a checkpoint N = 2560 108 -> 91, N = 2050
-// 247 -> 174 and N = 4097 248 -> 219, 8-bit output N = 5120 92 -> 84 and N = 2560
-// 98 -> 87; not at 5/8 (y N = 5120
-// 94 fitted, 85 fixed).
+// 247 -> 174 and N = 4097 248 -> 219, 8-bit output N = 5120 92 -> 84 and
+// N = 2560 98 -> 87; not at 5/8 for y (N = 5120 94 fitted, 85 fixed).
 int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
 {
     int s = 0;
@@ -112,7 +112,7 @@ int find_sched(int kind, bool packed, bool edge, int64_t nvec, bool many)
     if (!packed) {  // backward from here on
         if (full && !edge) return s;
         if (wide && half) return edge && nvec <= 512 ? gbn::kRowFit2 : gbn::kRowFit;
-        return four;
+        return many ? four : s;
     }
     if (!edge && many && !most) return four;
     if (wide && nvec <= 512) return (nvec + 63) / 64 * 32 < e.W ? gbn::kRowFit2 : s;
@@ -277,7 +277,8 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     if (sms <= 0) return GBN_EDEVICE;
     if (cscale) a.c = q8_of(nullptr, cscale, ct, N, group);
     gbn::RowPlan p{};
-    const bool fast = M > 0 && plan_rows(p, gbn::kKindB, xt, M, N, a.in, 3, {dx}, cscale != nullptr, 0, sms);
+    const bool fast =
+        M > 0 && plan_rows(p, gbn::kKindB, xt, M, N, a.in, 3, {dx}, cscale != nullptr, 0, sms);
     if (fast && !(p.fault = gbn::host_fault_ptr())) return GBN_EDEVICE;
     const int64_t P = M == 0 ? 0 : fast ? p.grid : gbn::add_bwd_general_rows(M, N, sms);
     if (dw && M > 0 && (!ws || ws_bytes < (size_t)P * (size_t)N * sizeof(float)))
@@ -292,9 +293,11 @@ int norm_backward(const void* s, const gbn_rows* sl, const float* cscale, int64_
     a.wt = wt;
     a.variant = variant;
     if (M > 0) {
-        const int mode = cscale ? (ct == gbn::kInt8 ? gbn::kBwdInt8 : gbn::kBwdC)
-                         : variant == GBN_RMS_CAST_FIRST ? (wt == xt ? gbn::kBwdCast16 : gbn::kBwdCast)
-                                                         : gbn::kBwdS;
+        const int mode = cscale && ct == gbn::kInt8         ? gbn::kBwdInt8
+                         : cscale                           ? gbn::kBwdC
+                         : variant != GBN_RMS_CAST_FIRST    ? gbn::kBwdS
+                         : wt == xt                         ? gbn::kBwdCast16
+                                                            : gbn::kBwdCast;
         const cudaError_t rc = !fast               ? gbn::launch_add_bwd_general(stream, xt, P, a)
                                : xt == gbn::kF32 ? gbn::launch_add_bwd_f32(stream, mode, a, p)
                                : xt == gbn::kF16 ? gbn::launch_add_bwd_f16(stream, mode, a, p)

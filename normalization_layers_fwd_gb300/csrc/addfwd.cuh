@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(row_sched(fwd_kind(kFull), S).T, row_minb(fwd_
                         // top): one atomic a run, whose order does not matter.
                         const bool out = shift && lane == 0;
                         float m = out ? 0.f : ma;
-                        for (int off = 1; off < lanes; off <<= 1)
-                            m = max_nan(m, __shfl_sync(0xffffffffu, m,
-                                                       ((((lane - shift) & (kIn - 1)) ^ off) + shift) &
-                                                           (kIn - 1),
-                                                       kIn));
+                        const int place = (lane - shift) & (kIn - 1);
+                        for (int off = 1; off < lanes; off <<= 1) {
+                            const int from = ((place ^ off) + shift) & (kIn - 1);
+                            m = max_nan(m, __shfl_sync(0xffffffffu, m, from, kIn));
+                        }
                         unsigned* const dst = gm + (half * R + g + u * G) * q8.ng + ga;
                         if (ok && ga >= 0 && (out || ((lane - shift) & (lanes - 1)) == 0))
                             atomicMax(dst, __float_as_uint(out ? ma : m));

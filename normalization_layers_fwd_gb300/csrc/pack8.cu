@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads)
             if (!ok[i]) continue;
             if constexpr (VEC == 8)
                 __stcs(reinterpret_cast<uint4*>(q) + v,
-                       make_uint4(q8_pack4<kType>(f[0], f[1], k, k), q8_pack4<kType>(f[2], f[3], k, k),
+                       make_uint4(q8_pack4<kType>(f[0], f[1], k, k),
+                                  q8_pack4<kType>(f[2], f[3], k, k),
                                   q8_pack4<kType>(g[0], g[1], k, k),
                                   q8_pack4<kType>(g[2], g[3], k, k)));
             else

@@ -394,8 +394,8 @@ __device__ __forceinline__ void load_weights(f2 (&wf)[KV][VEC / 2],
             if (wt == kF32) {
 #pragma unroll
                 for (int q = 0; q < P / 2; ++q) {
-                    const float4 v =
-                        __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c.col(j)) + q);
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(
+                        static_cast<const float*>(w) + c.col(j) + 4 * q));
                     wf[j][2 * q] = mk2(v.x, v.y);
                     wf[j][2 * q + 1] = mk2(v.z, v.w);
                 }

@@ -152,7 +152,8 @@ def add_rms_norm_quant(x, residual, weight, eps=1e-6, dtype=torch.float8_e4m3fn,
     stream s.  Without a gradient; call it where none is recorded."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                        for t in (x, residual, weight)):
-        raise RuntimeError("add_rms_norm_quant has no gradient: use add_rms_norm, or torch.no_grad()")
+        raise RuntimeError("add_rms_norm_quant has no gradient: use add_rms_norm, or call it under "
+                           "torch.no_grad()")
     q, scale, s, _ = _lib.rmsnorm_add_quant_fwd(x, residual, weight, eps, dtype, group,
                                                 save_rstd=False, variant=variant)
     return q, scale, s
